@@ -68,7 +68,8 @@ typedef enum {
     MACAQ_ETIMEOUT = -5,   /* a bounded device-side wait gave up (see macaq_device_status) */
     MACAQ_EWORKSPACE = -6, /* workspace smaller than the call needs */
     MACAQ_ETOOLARGE = -7,  /* problem needs more than the no-allocation scratch (below) */
-    MACAQ_ECOUNTS = -8     /* device routing counts were corrected or capped (macaq_w4a4_grouped_linear_device) */
+    MACAQ_ECOUNTS = -8,    /* device routing counts were corrected or capped (macaq_w4a4_grouped_linear_device) */
+    MACAQ_EINDEX = -9      /* a device-side position, slot, page or length was out of range (the cache calls) */
 } macaq_status;
 
 /* Human-readable name of a status code (static storage). */
@@ -340,9 +341,105 @@ int macaq_flip_refine(const float* W, int64_t N, int64_t K, const float* s, cons
                       const uint8_t* Ws, int64_t max_moves, int32_t* moves, void* workspace,
                       size_t workspace_bytes, void* stream);
 
+/*
+ * The attention path between the q/k/v projections and the o projection: norms and rotation of the
+ * heads, a paged key/value cache in MXFP4, and attention over it.  The stacked q/k/v call's output,
+ * bf16 [T][(Hq + 2 Hk) D], is what the first two read; attention's output [T][Hq D] is what the o
+ * projection's linear reads.
+ *
+ *   Heads.  head_dim D is 64 or 128; Hq and Hk <= 1024.  Rows are `ld` elements apart (a multiple of
+ *   8, at least the heads read).  Norm, each q and k head: y_d = x_d r w_d, r = 1 / sqrt(mean_d x_d^2 +
+ *   eps), weights fp32 [D] (NULL: no norm of those heads).  Rotation by row positions[t] of `rope`,
+ *   fp32 [rope_rows][rope_dim]: rope_dim/2 cosines, then as many sines; the first rope_dim (D or D/2)
+ *   elements of a head are rotated, (y_i, y_j) -> (y_i c - y_j s, y_j c + y_i s), with pairs (i, i +
+ *   rope_dim/2), or (2i, 2i+1) if interleaved = 1.  rope NULL: no rotation (positions unused).  All in
+ *   fp32, outputs rounded to bf16 once.
+ *
+ *   Cache.  uint8 [num_pages][Hk][macaq_kv4_page_bytes(page_size, D)], page_size P 16, 32, 64 or 128
+ *   tokens, 17 P D / 16 bytes per page and kv head.  It holds MXFP4 codes (rules as above) of
+ *   FWHT32(fl32(x c)), c = fl32(1/sqrt(32)), of keys after norm and rotation and of values: the same
+ *   block-Hadamard as the linears', which spreads outlier channels over their block.  With nb = D/32,
+ *   inside a page:
+ *     K codes   at 0:        token t, element 32b + 8c + j (j < 8): byte t D/2 + c 4nb + 4b + j/2
+ *     V codes   at P D/2:    token t, element 32b + 4g + j (j < 4): byte (t/2) D + g 4nb + (t%2) 2nb + 2b + j/2
+ *     K scales  at P D:      E8M0 byte of (t, b) at t nb + b
+ *     V scales  at P D + P nb, likewise            (even j in the low nibble)
+ *   so that attention's matrix fragments are contiguous 16-byte loads.  A token's bytes are its own: no
+ *   byte is shared between tokens.  Slot number = page * P + place in the page.  The bytes of a cache need
+ *   no initialisation: tokens past a sequence's length are never used.
+ *   An out-of-range index in device memory (a position outside the table, a slot or a page outside
+ *   the cache, a length past the table's pages, query ranges outside the rows) is skipped or cut,
+ *   never followed, and sets MACAQ_EINDEX in macaq_device_status.
+ *   These calls accept T = 0 (nothing is launched).
+ */
+size_t macaq_kv4_page_bytes(int page_size, int head_dim); /* 0 on invalid arguments */
+
+/*
+ * macaq_qk_norm_rope -- norm and rotation of the query and key heads in one pass.
+ *   qkv  in   bf16 [T] rows of Hq query heads, then Hk key heads (then anything)
+ *   q    out  bf16 [T][Hq][D];  k  out  bf16 [T][Hk][D]; they must not overlap qkv (either head count
+ *             may be 0, its output then unused)
+ *   eps >= 0; positions in, int64 [T].  A row whose position is outside the table is not written.
+ */
+int macaq_qk_norm_rope(const uint16_t* qkv, int64_t T, int64_t ld, int Hq, int Hk, int head_dim,
+                       const float* q_weight, const float* k_weight, float eps, const float* rope,
+                       int64_t rope_rows, int rope_dim, int interleaved, const int64_t* positions, uint16_t* q,
+                       uint16_t* k, void* stream);
+
+/*
+ * macaq_kv4_append -- store the keys and values of T tokens in the cache, norm, rotation, transform
+ * and quantisation on the way, and write the normed and rotated queries, in one launch.
+ *   qkv    in      bf16 [T] rows of Hq query, Hk key and Hk value heads (Hq = 0, q NULL: no queries)
+ *   cache  in/out  as above; only the bytes of the slots' tokens are written
+ *   slots  in      int64 [T]; negative: the row is padding, its key and value are not stored.  Two rows
+ *                  of one call must not name the same slot (its bytes would be a mix of both)
+ *   q      out     bf16 [T][Hq][D], written for padding rows too; not overlapping qkv
+ * The codes come from fp32 arithmetic in one canonical order, one rounding per operation: the sum of squares
+ * adds neighbours first (distances 1, 2, 4, .. D/2), y = fl(fl(x r) w), rotation fl(fl(y_i c) - fl(y_j s)).
+ */
+int macaq_kv4_append(const uint16_t* qkv, int64_t T, int64_t ld, int Hq, int Hk, int head_dim,
+                     const float* q_weight, const float* k_weight, float eps, const float* rope, int64_t rope_rows,
+                     int rope_dim, int interleaved, const int64_t* positions, uint8_t* cache, int64_t num_pages,
+                     int page_size, const int64_t* slots, uint16_t* q, void* stream);
+
+/*
+ * macaq_kv4_gather -- read tokens back: k, v out bf16 [T][Hk][D], the values that the cache holds for
+ * slots[t] (transformed back, rounded once); zeros for a negative slot or one outside the cache.
+ */
+int macaq_kv4_gather(const uint8_t* cache, int64_t num_pages, int page_size, int Hk, int head_dim,
+                     const int64_t* slots, int64_t T, uint16_t* k, uint16_t* v, void* stream);
+
+/*
+ * macaq_kv4_attention -- attention of query rows over the cache, o = softmax(scale q k^T) v.
+ *   q        in   bf16 [T] rows of Hq heads, ldq elements apart (after norm and rotation)
+ *   tables   in   int32 [B][table_width]: the pages of each sequence in order
+ *   kv_lens  in   int32 [B]: the keys of each sequence, its newest queries' own keys included
+ *   cu_q     in   int32 [B + 1]: sequence b's queries are rows cu_q[b] .. cu_q[b+1] - 1, its last tokens:
+ *                 query i of n stands at position kv_len - n + i.  NULL: one query per sequence, row b
+ *                 (B = T, max_q = 1)
+ *   max_q    in   the most queries of any sequence, known on the host; it picks the kernels.  A longer
+ *                 sequence's rows past it are not written (MACAQ_EINDEX)
+ *   scale    in   finite and > 0;  window in: 0, or the number of newest keys a query sees, its own included
+ *   out      out  bf16 [T][Hq][D]; rows outside every sequence are left as they were
+ *   lse      out  fp32 [T][Hq], the natural logarithm of the sum of exp(scale q k); NULL: not wanted
+ *   workspace in  macaq_kv4_attention_workspace_bytes(...) bytes; contents on entry and on return
+ *                 unspecified; calls sharing it must be stream-ordered
+ * Head h reads kv head h / (Hq / Hk).  Query i sees keys j <= its position, and with a window those
+ * above position - window; a query that sees none (kv_len 0, or fewer keys than queries) gets
+ * zeros and lse -inf.  Softmax statistics and sums are fp32.  Results do not depend on what the pages
+ * hold behind a sequence's length, and are the same from run to run.
+ */
+size_t macaq_kv4_attention_workspace_bytes(int64_t T, int64_t B, int Hq, int Hk, int head_dim, int64_t max_q);
+int macaq_kv4_attention(const uint16_t* q, int64_t T, int64_t ldq, int Hq, int Hk, int head_dim,
+                        const uint8_t* cache, int64_t num_pages, int page_size, const int32_t* tables, int64_t B,
+                        int64_t table_width, const int32_t* kv_lens, const int32_t* cu_q, int64_t max_q, float scale,
+                        int64_t window, uint16_t* out, float* lse, void* workspace, size_t workspace_bytes,
+                        void* stream);
+
 /* Sticky device-side status of the current device: MACAQ_OK; MACAQ_ETIMEOUT once a bounded
- * wait inside a kernel gave up; MACAQ_ECOUNTS once device routing counts had to be corrected (the
- * last event recorded wins).  Synchronises the device.  `clear` != 0 resets it. */
+ * wait inside a kernel gave up; MACAQ_ECOUNTS once device routing counts had to be corrected;
+ * MACAQ_EINDEX once a device-side index of the cache calls was out of range (the last event recorded
+ * wins).  Synchronises the device.  `clear` != 0 resets it. */
 int macaq_device_status(int clear);
 
 #ifdef __cplusplus

@@ -30,6 +30,8 @@ __all__ = [
     "grouped_workspace_bytes", "macaq_w4a4_linear_noalloc", "macaq_calib_hessian", "macaq_flip_refine",
     "macaq_w4a4_grouped_linear_device", "grouped_device_workspace_bytes", "macaq_scales_to_tiled",
     "macaq_scales_to_rowmajor", "macaq_w4a4_linear_multi", "linear_multi_workspace_bytes",
+    "macaq_qk_norm_rope", "macaq_kv4_append", "macaq_kv4_gather", "macaq_kv4_attention", "kv4_page_bytes",
+    "kv4_attention_workspace_bytes",
     "macaq_device_status", "status_str", "EXPORTED_SYMBOLS",
 ]
 
@@ -43,7 +45,8 @@ EXPORTED_SYMBOLS = (
     "macaq_hessian_workspace_bytes", "macaq_calib_hessian", "macaq_flip_refine_workspace_bytes",
     "macaq_flip_refine", "macaq_grouped_device_workspace_bytes", "macaq_w4a4_grouped_linear_device",
     "macaq_scales_to_tiled", "macaq_scales_to_rowmajor", "macaq_linear_multi_workspace_bytes",
-    "macaq_w4a4_linear_multi",
+    "macaq_w4a4_linear_multi", "macaq_kv4_page_bytes", "macaq_qk_norm_rope", "macaq_kv4_append",
+    "macaq_kv4_gather", "macaq_kv4_attention_workspace_bytes", "macaq_kv4_attention",
 )
 
 MACAQ_OK = 0
@@ -105,11 +108,23 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
         lib.macaq_linear_multi_workspace_bytes.argtypes = [i64, i32, i64]
         lib.macaq_linear_multi_workspace_bytes.restype = sz
         lib.macaq_w4a4_linear_multi.argtypes = [p, i64, i64, i32, p, p, p, p, p, p, sz, p]
+        f32 = ctypes.c_float
+        lib.macaq_kv4_page_bytes.argtypes = [i32, i32]
+        lib.macaq_kv4_page_bytes.restype = sz
+        lib.macaq_qk_norm_rope.argtypes = [p, i64, i64, i32, i32, i32, p, p, f32, p, i64, i32, i32, p, p, p, p]
+        lib.macaq_kv4_append.argtypes = [p, i64, i64, i32, i32, i32, p, p, f32, p, i64, i32, i32, p, p, i64, i32, p,
+                                         p, p]
+        lib.macaq_kv4_gather.argtypes = [p, i64, i32, i32, i32, p, i64, p, p, p]
+        lib.macaq_kv4_attention_workspace_bytes.argtypes = [i64, i64, i32, i32, i32, i64]
+        lib.macaq_kv4_attention_workspace_bytes.restype = sz
+        lib.macaq_kv4_attention.argtypes = [p, i64, i64, i32, i32, i32, p, i64, i32, p, i64, i64, p, p, i64, f32, i64,
+                                            p, p, p, sz, p]
         for name in ("macaq_calibrate_scale", "macaq_fold_weights", "macaq_act_transform_quant", "macaq_act_quant_plain",
                      "macaq_mxfp4_gemm", "macaq_w4a4_linear", "macaq_mxfp4_linear", "macaq_device_status",
                      "macaq_w4a4_grouped_linear", "macaq_w4a4_linear_noalloc", "macaq_calib_hessian",
                      "macaq_flip_refine", "macaq_w4a4_grouped_linear_device", "macaq_scales_to_tiled",
-                     "macaq_scales_to_rowmajor", "macaq_w4a4_linear_multi"):
+                     "macaq_scales_to_rowmajor", "macaq_w4a4_linear_multi", "macaq_qk_norm_rope", "macaq_kv4_append",
+                     "macaq_kv4_gather", "macaq_kv4_attention"):
             getattr(lib, name).restype = i32
         if path is None:
             _lib = lib
@@ -537,7 +552,179 @@ def macaq_flip_refine(W: torch.Tensor, s: torch.Tensor, Hs: torch.Tensor, Wq: to
     return moves
 
 
+def _need_rows(t: torch.Tensor, name: str, width: int, device=None) -> int:
+    """A bf16 CUDA tensor [T, >= width] whose rows are contiguous and may lie further apart (a slice of
+    the columns of a stacked output); returns the distance between rows in elements."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the call's other tensors on {device}")
+    if t.dtype != torch.bfloat16:
+        raise ValueError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if t.dim() != 2 or t.shape[1] < width:
+        raise ValueError(f"{name} must have shape (T, {width} or more), got {tuple(t.shape)}")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"the rows of {name} must be contiguous")
+    ld = t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    if ld < t.shape[1]:
+        raise ValueError(f"the rows of {name} overlap")
+    if ld % 8:
+        if t.shape[0] > 1:
+            raise ValueError(f"the rows of {name} must lie a multiple of 8 elements apart, got {ld}")
+        ld += 8 - ld % 8  # a single row: nothing lies behind it
+    return ld
+
+
+def _rope_args(rope, positions, head_dim: int, T: int, device):
+    """(rope_rows, rope_dim) after the checks of a rotation table and positions."""
+    if rope is None:
+        return 0, 0
+    _need(rope, "rope", torch.float32, device=device)
+    if rope.dim() != 2 or rope.shape[1] not in (head_dim, head_dim // 2):
+        raise ValueError(f"rope must have shape (positions, {head_dim} or {head_dim // 2}), got {tuple(rope.shape)}")
+    if positions is None:
+        raise ValueError("rope needs positions")
+    _need(positions, "positions", torch.int64, (T,), device=device)
+    return rope.shape[0], rope.shape[1]
+
+
+def kv4_page_bytes(page_size: int, head_dim: int) -> int:
+    """Bytes of one page of one kv head: allocate the cache as uint8 [pages, Hk, kv4_page_bytes(...)]."""
+    return int(load_library().macaq_kv4_page_bytes(page_size, head_dim))
+
+
+def _need_cache(cache, page_size: int, head_dim: int, device=None):
+    """(pages, kv heads) of a cache tensor."""
+    pb = kv4_page_bytes(page_size, head_dim)
+    if pb == 0:
+        raise ValueError(f"page_size must be 16, 32, 64 or 128 and head_dim 64 or 128, got {page_size}, {head_dim}")
+    _need(cache, "cache", torch.uint8, device=device)
+    if cache.dim() != 3 or cache.shape[2] != pb:
+        raise ValueError(f"cache must have shape (pages, kv heads, {pb}), got {tuple(cache.shape)}")
+    return cache.shape[0], cache.shape[1]
+
+
+def macaq_qk_norm_rope(qkv: torch.Tensor, Hq: int, Hk: int, head_dim: int, rope=None, positions=None, q_weight=None,
+                       k_weight=None, eps: float = 1e-6, interleaved: bool = False, q=None, k=None, stream=None):
+    """Per-head norm (weights fp32 [head_dim], None: none) and position rotation of the query and key
+    heads of qkv (bf16 [T, (Hq + Hk) * head_dim or more], e.g. the stacked q/k/v output) in one pass.
+    rope fp32 [P, R]: R/2 cosines then R/2 sines of each position, R = head_dim or head_dim/2; positions
+    int64 [T].  Returns (q [T, Hq, head_dim], k [T, Hk, head_dim]) in bf16."""
+    ld = _need_rows(qkv, "qkv", (Hq + Hk) * head_dim)
+    dev, T = qkv.device, qkv.shape[0]
+    rows, R = _rope_args(rope, positions, head_dim, T, dev)
+    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is not None:
+            _need(w, name, torch.float32, (head_dim,), device=dev)
+    q = torch.empty(T, Hq, head_dim, dtype=torch.bfloat16, device=dev) if q is None else q
+    k = torch.empty(T, Hk, head_dim, dtype=torch.bfloat16, device=dev) if k is None else k
+    _need(q, "q", torch.bfloat16, (T, Hq, head_dim), device=dev)
+    _need(k, "k", torch.bfloat16, (T, Hk, head_dim), device=dev)
+    with torch.cuda.device(dev):
+        _check(load_library().macaq_qk_norm_rope(_ptr(qkv), T, ld, Hq, Hk, head_dim, _ptr(q_weight), _ptr(k_weight),
+                                                 eps, _ptr(rope), rows, R, 1 if interleaved else 0, _ptr(positions),
+                                                 _ptr(q), _ptr(k), _stream(stream, dev)), "macaq_qk_norm_rope")
+    return q, k
+
+
+def macaq_kv4_append(qkv: torch.Tensor, Hq: int, Hk: int, head_dim: int, cache: torch.Tensor, page_size: int,
+                     slots: torch.Tensor, rope=None, positions=None, q_weight=None, k_weight=None, eps: float = 1e-6,
+                     interleaved: bool = False, q=None, stream=None):
+    """Stores the keys and values of qkv (bf16 [T, (Hq + 2 Hk) * head_dim or more]) in the paged MXFP4
+    cache (uint8 [pages, Hk, kv4_page_bytes(page_size, head_dim)]) at slots (int64 [T], page * page_size
+    + place; negative: padding, not stored), with norm and rotation (as macaq_qk_norm_rope), transform and
+    quantisation on the way.  Returns the normed and rotated queries, bf16 [T, Hq, head_dim] (Hq = 0:
+    None)."""
+    ld = _need_rows(qkv, "qkv", (Hq + 2 * Hk) * head_dim)
+    dev, T = qkv.device, qkv.shape[0]
+    pages, heads = _need_cache(cache, page_size, head_dim, dev)
+    if heads != Hk:
+        raise ValueError(f"cache holds {heads} kv heads, the call names {Hk}")
+    _need(slots, "slots", torch.int64, (T,), device=dev)
+    rows, R = _rope_args(rope, positions, head_dim, T, dev)
+    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is not None:
+            _need(w, name, torch.float32, (head_dim,), device=dev)
+    if Hq:
+        q = torch.empty(T, Hq, head_dim, dtype=torch.bfloat16, device=dev) if q is None else q
+        _need(q, "q", torch.bfloat16, (T, Hq, head_dim), device=dev)
+    with torch.cuda.device(dev):
+        _check(load_library().macaq_kv4_append(_ptr(qkv), T, ld, Hq, Hk, head_dim, _ptr(q_weight), _ptr(k_weight), eps,
+                                               _ptr(rope), rows, R, 1 if interleaved else 0, _ptr(positions),
+                                               _ptr(cache), pages, page_size, _ptr(slots), _ptr(q) if Hq else None,
+                                               _stream(stream, dev)), "macaq_kv4_append")
+    return q if Hq else None
+
+
+def macaq_kv4_gather(cache: torch.Tensor, head_dim: int, page_size: int, slots: torch.Tensor, k=None, v=None,
+                     stream=None):
+    """Reads tokens back from the cache: (k, v) bf16 [T, Hk, head_dim], the values it holds for slots
+    (int64 [T]); zeros for negative slots."""
+    pages, Hk = _need_cache(cache, page_size, head_dim)
+    dev = cache.device
+    T = slots.numel()
+    _need(slots, "slots", torch.int64, (T,), device=dev)
+    k = torch.empty(T, Hk, head_dim, dtype=torch.bfloat16, device=dev) if k is None else k
+    v = torch.empty(T, Hk, head_dim, dtype=torch.bfloat16, device=dev) if v is None else v
+    _need(k, "k", torch.bfloat16, (T, Hk, head_dim), device=dev)
+    _need(v, "v", torch.bfloat16, (T, Hk, head_dim), device=dev)
+    with torch.cuda.device(dev):
+        _check(load_library().macaq_kv4_gather(_ptr(cache), pages, page_size, Hk, head_dim, _ptr(slots), T, _ptr(k),
+                                               _ptr(v), _stream(stream, dev)), "macaq_kv4_gather")
+    return k, v
+
+
+def kv4_attention_workspace_bytes(T: int, B: int, Hq: int, Hk: int, head_dim: int, max_q: int, device=None) -> int:
+    """Scratch bytes macaq_kv4_attention needs for T query rows of B sequences on `device` (default: the
+    current one; the size depends on its SM count)."""
+    with _device(device):
+        return int(load_library().macaq_kv4_attention_workspace_bytes(T, B, Hq, Hk, head_dim, max_q))
+
+
+def macaq_kv4_attention(q: torch.Tensor, cache: torch.Tensor, page_size: int, tables: torch.Tensor,
+                        kv_lens: torch.Tensor, cu_q=None, max_q: int = 1, scale: float | None = None, window: int = 0,
+                        out=None, lse=None, workspace=None, stream=None):
+    """Attention of q (bf16 [T, Hq, head_dim], rows may lie further apart) over the paged MXFP4 cache,
+    causal: tables int32 [B, pages of a sequence], kv_lens int32 [B] keys of each sequence, cu_q int32
+    [B + 1] its query rows (None: one query each), max_q the most queries of any sequence, scale (default
+    head_dim ** -0.5), window (0: none) the newest keys a query sees.  Returns out bf16 [T, Hq, head_dim];
+    lse, if given (fp32 [T, Hq]), receives the logarithms of the softmax sums."""
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise ValueError("q must be a CUDA tensor of shape (T, heads, head_dim)")
+    T, Hq, D = q.shape
+    if T and (q.stride(2) != 1 or (Hq > 1 and q.stride(1) != D)):
+        raise ValueError("the rows of q must be contiguous")
+    ld = _need_rows(q.as_strided((T, Hq * D), (q.stride(0), 1)), "q", Hq * D)
+    dev = q.device
+    pages, Hk = _need_cache(cache, page_size, D, dev)
+    if not isinstance(tables, torch.Tensor) or tables.dim() != 2:
+        raise ValueError("tables must be a CUDA tensor of shape (sequences, pages)")
+    B, width = tables.shape
+    _need(tables, "tables", torch.int32, device=dev)
+    _need(kv_lens, "kv_lens", torch.int32, (B,), device=dev)
+    if cu_q is not None:
+        _need(cu_q, "cu_q", torch.int32, (B + 1,), device=dev)
+    elif B != T or max_q != 1:
+        raise ValueError("without cu_q every sequence has one query: T = B and max_q = 1")
+    out = torch.empty(T, Hq, D, dtype=torch.bfloat16, device=dev) if out is None else out
+    _need(out, "out", torch.bfloat16, (T, Hq, D), device=dev)
+    if lse is not None:
+        _need(lse, "lse", torch.float32, (T, Hq), device=dev)
+    need = kv4_attention_workspace_bytes(T, B, Hq, Hk, D, max_q, dev)
+    if need == 0:
+        raise ValueError("shape not supported by the attention (Hq a multiple of Hk, at most 1024; max_q >= 1)")
+    workspace = torch.empty(need, dtype=torch.uint8, device=dev) if workspace is None else workspace
+    _need(workspace, "workspace", torch.uint8, min_numel=need, device=dev)
+    with torch.cuda.device(dev):
+        _check(load_library().macaq_kv4_attention(
+            _ptr(q), T, ld, Hq, Hk, D, _ptr(cache), pages, page_size, _ptr(tables), B, width, _ptr(kv_lens), _ptr(cu_q),
+            int(max_q), D ** -0.5 if scale is None else float(scale), int(window), _ptr(out), _ptr(lse),
+            _ptr(workspace), workspace.numel(), _stream(stream, dev)), "macaq_kv4_attention")
+    return out
+
+
 def macaq_device_status(clear: bool = False) -> int:
-    """MACAQ_OK, or the last device-side event: MACAQ_ETIMEOUT (a bounded wait gave up) or
-    MACAQ_ECOUNTS (device routing counts were corrected).  Synchronises."""
+    """MACAQ_OK, or the last device-side event: MACAQ_ETIMEOUT (a bounded wait gave up), MACAQ_ECOUNTS
+    (device routing counts were corrected) or MACAQ_EINDEX (an index of a cache call was out of range).
+    Synchronises."""
     return int(load_library().macaq_device_status(1 if clear else 0))

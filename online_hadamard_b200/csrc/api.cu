@@ -35,6 +35,8 @@ extern "C" const char* macaq_status_str(int status) {
             return "MACAQ_ETOOLARGE: problem needs more scratch than the no-allocation entry point holds";
         case MACAQ_ECOUNTS:
             return "MACAQ_ECOUNTS: device routing counts were negative or ran past the rows of x (corrected)";
+        case MACAQ_EINDEX:
+            return "MACAQ_EINDEX: a device-side position, slot, page or length was out of range (skipped or cut)";
         default: return "MACAQ: unknown status";
     }
 }
@@ -98,5 +100,5 @@ extern "C" int macaq_device_status(int clear) {
         const int zero = 0;
         if (cudaMemcpyToSymbol(g_device_status, &zero, sizeof(int)) != cudaSuccess) return MACAQ_ECUDA;
     }
-    return v;  // MACAQ_OK, or the code of the last event recorded (MACAQ_ETIMEOUT, MACAQ_ECOUNTS)
+    return v;  // MACAQ_OK, or the code of the last event recorded (MACAQ_ETIMEOUT, MACAQ_ECOUNTS, MACAQ_EINDEX)
 }

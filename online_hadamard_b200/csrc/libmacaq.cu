@@ -6,3 +6,5 @@
 #include "gemm.cu"
 #include "noalloc.cu"
 #include "calib.cu"
+#include "kvcache.cu"
+#include "attend.cu"
