@@ -407,12 +407,10 @@ __global__ void __launch_bounds__(kHeadThreads) heads_kernel(const __grid_consta
 
 // Eight E2M1 codes of a word (element j in nibble j) as floats.
 __device__ __forceinline__ void decode_e2m1x8(uint32_t w, float* f) {
+    const uint32_t h[4] = {e2m1x2_to_f16x2<0>(w), e2m1x2_to_f16x2<1>(w), e2m1x2_to_f16x2<2>(w), e2m1x2_to_f16x2<3>(w)};
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        uint32_t h2;
-        asm("{\n\t.reg .b8 b0;\n\tcvt.u8.u32 b0, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, b0;\n\t}" : "=r"(h2) : "r"(w >> (8 * j)));
-        const __half2 h = *reinterpret_cast<const __half2*>(&h2);
-        const float2 v = __half22float2(h);
+        const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&h[j]));
         f[2 * j] = v.x, f[2 * j + 1] = v.y;
     }
 }

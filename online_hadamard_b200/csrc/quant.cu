@@ -317,10 +317,11 @@ __global__ void __launch_bounds__(kQuantThreads, 4) mx_quant_grouped_kernel(
 // dependency wait, apart from the device-built expert table, whose quantiser is therefore launched
 // in plain stream order (launch_act_quant_grouped_device).
 template <class Kern, class... Args>
-static int launch_dependent(Kern kernel, dim3 grid, dim3 block, cudaStream_t stream, Args... args) {
+static int launch_dependent_smem(Kern kernel, dim3 grid, dim3 block, size_t smem, cudaStream_t stream, Args... args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -329,6 +330,10 @@ static int launch_dependent(Kern kernel, dim3 grid, dim3 block, cudaStream_t str
     cfg.numAttrs = 1;
     if (cudaLaunchKernelEx(&cfg, kernel, args...) != cudaSuccess) return MACAQ_ECUDA;
     return launch_status();
+}
+template <class Kern, class... Args>
+static int launch_dependent(Kern kernel, dim3 grid, dim3 block, cudaStream_t stream, Args... args) {
+    return launch_dependent_smem(kernel, grid, block, 0, stream, args...);
 }
 
 // Rows per thread: enough threads to fill the GPU, rows walked by each otherwise.
