@@ -40,11 +40,11 @@ struct AttendParams {
     int window;        // 0: none
     uint16_t* out;     // bf16 [T][Hq][D]
     float* lse;        // fp32 [T][Hq] or null
-    // the split of the work (plan_attend): row tiles of tile_rows rows, each cut along its keys into
-    // at most `splits` parts whose results are joined by attend_join_kernel (splits = 1: written directly)
-    int tile_rows, row_tiles, splits;
-    float* part_o;    // fp32 [splits][units][tile_rows][D], each row divided by its own sum
-    float2* part_ml;  // [splits][units][tile_rows]: its reference m (base 2) and sum of 2^(s - m)
+    // the split of the work (plan_attend): row tiles of tile_rows rows; `ctas` > 0: all blocks of keys of
+    // all units in one row, cut into that many equal lengths (Cut); 0: one CTA per unit
+    int tile_rows, row_tiles, ctas;
+    float* part_o;    // fp32 [ctas][2][tile_rows][D], each row divided by its own sum
+    float2* part_ml;  // [ctas][2][tile_rows]: its reference m (base 2) and sum of 2^(s - m)
 };
 
 // Sequence b: its first query row, its queries, its keys and its first query's position (negative
@@ -81,18 +81,74 @@ __device__ __forceinline__ Span span_of(const AttendParams& p, const Sequence& s
     return {first_key(p, a), first_key(p, z), a, z};
 }
 
-// Part `split` of a span in blocks of 2^shift keys: blocks [begin, end) of it, of `parts` parts in use.
-// No part is shorter than kMinKeys keys (a shorter one costs more to join than it saves).
+// A unit is a (sequence, kv head, tile of query rows); its work is its span in blocks of 2^shift keys.
+__device__ __forceinline__ int blocks_of(const Span& sp, int shift) {
+    return sp.last_hi < 0 ? 0 : (sp.last_hi >> shift) - (sp.first_lo >> shift) + 1;
+}
+// Blocks of all row tiles of one kv head of a sequence.
+__device__ __forceinline__ int64_t sequence_blocks(const AttendParams& p, const Sequence& s, int shift) {
+    int64_t n = 0;
+    const int rows = s.nq * p.G;
+    for (int r0 = 0; r0 < rows; r0 += p.tile_rows) n += blocks_of(span_of(p, s, r0, min(p.tile_rows, rows - r0)), shift);
+    return n;
+}
+
+// Sequences are of unequal length, known on the device only, and few units leave most of the GPU idle: so
+// the blocks of all units stand in one row (sequence, then kv head, then row tile), and CTA i of the
+// resident ones takes [i len, (i + 1) len) of it, whatever units those belong to.  A unit that one CTA holds
+// whole is written directly, parts of one are joined by attend_join_kernel.  A CTA cuts at most two units:
+// its parts go to slot 0 (the unit that its range begins in) and slot 1 (the one it ends in).  No CTA gets
+// less than kMinKeys keys (joining would cost more than it saves).
 constexpr int kMinKeys = 128;
-struct Part {
-    int begin, end, parts;
+__device__ __forceinline__ int64_t cut_length(const AttendParams& p, int64_t total, int shift) {
+    const int64_t len = (total + p.ctas - 1) / p.ctas;
+    return len > (kMinKeys >> shift) ? len : (kMinKeys >> shift);
+}
+
+struct Cut {
+    int64_t pos, end;  // this CTA's range
+    int b;             // the sequence that pos lies in, and where that sequence begins
+    int64_t seq_pos;
 };
-__device__ __forceinline__ Part part_of(const AttendParams& p, const Span& sp, int shift, int split) {
-    if (sp.last_hi < 0) return {0, 0, 0};
-    const int b0 = sp.first_lo >> shift, n = (sp.last_hi >> shift) - b0 + 1;
-    const int len = max((n + p.splits - 1) / p.splits, kMinKeys >> shift);
-    const int begin = min(n, split * len);
-    return {b0 + begin, b0 + min(n, begin + len), (n + len - 1) / len};
+// By all 128 threads of a CTA: thread i adds up its share of the sequences, the one whose share holds the
+// CTA's first block walks it.
+__device__ __forceinline__ Cut cut_of(const AttendParams& p, int shift, int64_t* scan, int* first_seq, int64_t* first_pos) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int share = (p.B + 127) / 128, b0 = min(p.B, static_cast<int>(threadIdx.x) * share), b1 = min(p.B, b0 + share);
+    int64_t mine = 0;
+    for (int b = b0; b < b1; ++b) mine += sequence_blocks(p, sequence_of(p, b), shift) * p.Hk;
+    int64_t upto = mine;
+#pragma unroll
+    for (int x = 1; x < 32; x <<= 1) {
+        const int64_t y = __shfl_up_sync(0xFFFFFFFFu, upto, x);
+        if (lane >= x) upto += y;
+    }
+    if (lane == 31) scan[warp] = upto;
+    __syncthreads();
+    int64_t total = 0;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+        if (w < warp) upto += scan[w];
+        total += scan[w];
+    }
+    const int64_t len = cut_length(p, total, shift);
+    Cut c;
+    c.pos = static_cast<int64_t>(blockIdx.x) * len;
+    c.end = c.pos + len < total ? c.pos + len : total;
+    if (c.pos < upto && c.pos >= upto - mine) {
+        int64_t at = upto - mine;
+        for (int b = b0; b < b1; ++b) {
+            const int64_t n = sequence_blocks(p, sequence_of(p, b), shift) * p.Hk;
+            if (c.pos < at + n) {
+                *first_seq = b, *first_pos = at;
+                break;
+            }
+            at += n;
+        }
+    }
+    __syncthreads();
+    c.b = *first_seq, c.seq_pos = *first_pos;
+    return c;
 }
 
 // Query rows are brought to f16 by a power of two of their own: |q| < 2^(E - 126) for the row's largest
@@ -124,16 +180,16 @@ constexpr float kLift = 6.0f;
 
 // --------------------------------------------------------------------------- few query rows
 //
-// One CTA of 4 warps per (sequence, kv head, tile of 8 NT rows, part of the keys).  A warp takes strips
-// of 16 tokens: S^T = K Q^T (m = 16 tokens, n = 8 rows) and O^T += V^T P^T (m = 16 elements, k = 16
-// tokens) by warp-level matrix instructions, which need 8 rows only where the 128-row tcgen05 tiles would
-// be nearly empty.  Codes go from shared memory straight into fragments (the cache's layout is theirs:
-// 16-byte loads, no shuffle) and are widened to f16 exactly; K's block scales multiply the partial sums of
-// their block, V's the softmax weights, relative to the largest scale a warp has met.  Each warp copies its
-// own strips, kStages deep, with nothing shared until the end, where the warps' sums are joined.
-// Bound by the cache's bytes at long contexts; the work of widening (a conversion per two codes) comes next.
+// CTAs of 4 warps.  A warp takes blocks of 32 tokens, as two strips of 16: S^T = K Q^T (m = 16 tokens,
+// n = 8 rows) and O^T += V^T P^T (m = 16 elements, k = 16 tokens) by warp-level matrix instructions, which
+// need 8 rows only where the 128-row tcgen05 tiles would be nearly empty.  Codes go from shared memory
+// straight into fragments (the cache's layout is theirs: 16-byte loads, no shuffle) and are widened to f16
+// exactly; K's block scales multiply the partial sums of their block, V's the softmax weights, relative to the
+// largest scale a warp has met.  Each warp copies its own blocks, kStages deep, with nothing shared
+// until the end, where the warps' sums are joined.
 constexpr int kFewThreads = 128;
-constexpr int kStages = 4;
+constexpr int kStages = 3;
+constexpr int kFewShift = 5;
 
 template <int D>
 struct Strip {
@@ -148,76 +204,86 @@ struct Strip {
     }
 };
 
-template <int D, int NT>
-__global__ void __launch_bounds__(kFewThreads) attend_few_kernel(const __grid_constant__ AttendParams p) {
-    using S = Strip<D>;
-    constexpr int kBlocks = D / 32, kRows = 8 * NT, kQStride = D + 8;
-    extern __shared__ uint4 dynamic_smem[];
-    __shared__ __align__(16) __half q_s[kRows][kQStride];
-    __shared__ float factor_s[kRows];
-    __shared__ int lo_s[kRows], hi_s[kRows];
-    __shared__ float2 ml_s[4][8];
-    __shared__ float vref_s[4];
+// CTAs of an SM: what its registers hold (168 a thread, 255 with 32 rows).
+constexpr int few_resident(int NT) { return NT == 4 ? 2 : 3; }
 
-    griddep_launch_dependents();
-    griddep_wait();
+template <int D, int NT>
+struct FewShared {
+    static constexpr int kBlocks = D / 32;
+    static constexpr size_t kRing = 4 * kStages * 2 * Strip<D>::kBytes, kJoin = 4 * 8 * D * sizeof(float);
+    alignas(16) uint8_t ring[kRing > kJoin ? kRing : kJoin];  // in the end the warps' sums of 8 rows
+    alignas(16) __half q[8 * NT][D + 8];
+    alignas(16) float kscale[4][2][16][kBlocks];    // a warp's strips: 2^(e - 127) of K's blocks
+    alignas(16) uint32_t vscale[4][2][8][kBlocks];  // f16 2^(e - vref) of V's, two tokens
+    float factor[8 * NT];
+    int lo[8 * NT], hi[8 * NT];
+    float2 ml[4][8];
+    float vref[4];
+    int64_t scan[4];
+    int first_seq;
+    int64_t first_pos;
+};
+
+// One unit, blocks [begin, end) of its span (absolute block numbers); slot < 0: the result itself.
+template <int D, int NT>
+__device__ __forceinline__ void few_unit(const AttendParams& p, FewShared<D, NT>& sm, const Sequence& s, int b, int kvh,
+                                         int r0, int nrows, const Span& sp, int begin, int end, int64_t slot) {
+    using S = Strip<D>;
+    constexpr int kBlocks = D / 32, kRows = 8 * NT;
+    constexpr int kSub = NT == 4 ? 1 : 2;  // strips worked on together, as registers allow
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = lane >> 2, c = lane & 3;
-    const int64_t block = blockIdx.x;
-    const int rt = static_cast<int>(block % p.row_tiles);
-    const int split = static_cast<int>(block / p.row_tiles % p.splits);
-    const int64_t bh = block / p.row_tiles / p.splits;
-    const int kvh = static_cast<int>(bh % p.Hk), b = static_cast<int>(bh / p.Hk);
-    const Sequence s = sequence_of(p, b);
-    const int r0 = rt * kRows;
-    const int nrows = min(kRows, s.nq * p.G - r0);
-    if (nrows <= 0) return;
-    const Span sp = span_of(p, s, r0, nrows);
-    const Part part = part_of(p, sp, 4, split);
-    if (p.splits > 1 && part.begin >= part.end) return;
-
-    const int count = max(0, (part.end - part.begin - warp + 3) >> 2);  // strips of this warp
-    const PageLayout<D> lay{p.page_size};
+    const int count = max(0, (end - begin - warp + 3) >> 2);  // blocks of this warp
     const int32_t* table = p.tables + b * p.table_width;
-    uint8_t* ring = reinterpret_cast<uint8_t*>(dynamic_smem) + warp * kStages * S::kBytes;
-    unsigned bad = 0;  // stages whose page lies outside the cache
-    auto page_of = [&](int i) { return i < count ? table[((part.begin + warp + 4 * i) * 16) >> p.page_shift] : 0; };
-    auto fetch = [&](int i, int32_t pg) {
-        if (i < count) {
-            const int stage = i % kStages;
-            const bool ok = pg >= 0 && pg < p.num_pages;
-            bad = (bad & ~(1u << stage)) | (ok ? 0u : 1u << stage);
-            if (ok) {
-                const int at = ((part.begin + warp + 4 * i) * 16) & (p.page_size - 1);
-                const uint8_t* page = p.cache + (static_cast<int64_t>(pg) * p.Hk + kvh) * lay.bytes();
-                const uint8_t* kc = page + at * lay.kRow;
-                const uint8_t* vc = page + lay.v_codes() + (at >> 1) * D;
-                uint8_t* dst = ring + stage * S::kBytes;
+    uint8_t* ring = sm.ring + warp * kStages * 2 * S::kBytes;
+    unsigned gone_bits = 0;  // bits 2 stage + u: strips that were not copied
+    // what a lane copies: 16 bytes (D = 128: 32) of K and of V codes, and a piece of the scales
+    const PageLayout<D> lay{p.page_size};
+    const uint8_t* head = p.cache + kvh * lay.bytes();
+    const uint32_t page_stride = static_cast<uint32_t>(p.Hk * lay.bytes());
+    const int scale_at = lane < kBlocks ? lay.k_scales() + 16 * lane : lay.v_scales() + 16 * (lane - kBlocks);
+    const uint32_t ring_at = smem_u32(ring) + 16 * lane;
+    const uint32_t v_at = smem_u32(ring) + S::kV + 16 * S::v_piece(lane / (D / 16), lane % (D / 16));
+    int ahead = (begin + warp) * 32;                 // first token of the block to fetch next
+    const int fetch_end = end * 32;
+    auto page_of = [&](int t) {  // -1: nothing of the strip is seen
+        return t < fetch_end && t <= sp.last_hi && t + 15 >= sp.first_lo ? table[t >> p.page_shift] : -1;
+    };
+    auto fetch = [&](unsigned stage, int pg0, int pg1) {
+        if (ahead < fetch_end) {
 #pragma unroll
-                for (int u = 0; u < D / 64; ++u) {
-                    const int x = lane + 32 * u;
-                    cp_async16(dst + 16 * x, kc + 16 * x);
-                    cp_async16(dst + S::kV + 16 * S::v_piece(x / (D / 16), x % (D / 16)), vc + 16 * x);
+            for (int u = 0; u < 2; ++u) {
+                const int pg = u ? pg1 : pg0, t = ahead + 16 * u;
+                const unsigned bit = 1u << (2 * stage + u);
+                gone_bits |= bit;
+                if (static_cast<unsigned>(pg) < static_cast<uint64_t>(p.num_pages)) {
+                    gone_bits &= ~bit;
+                    const int at = t & (p.page_size - 1);
+                    const uint8_t* page = head + static_cast<uint64_t>(static_cast<uint32_t>(pg)) * page_stride;
+                    const uint8_t* kc = page + (at * lay.kRow + 16 * lane);  // V's pair rows lie as far apart as two K rows
+                    const uint8_t* vc = kc + lay.v_codes();
+                    const uint32_t to = (2 * stage + u) * S::kBytes;
+#pragma unroll
+                    for (int x = 0; x < D / 64; ++x) {
+                        cp_async16(ring_at + to + 512 * x, kc + 512 * x);
+                        cp_async16(v_at + to + 512 * x, vc + 512 * x);
+                    }
+                    if (lane < 2 * kBlocks) cp_async16(ring_at + to + S::kKs, page + (scale_at + at * kBlocks));
+                } else if (lane == 0 && t <= sp.last_hi && t + 15 >= sp.first_lo) {
+                    report_index();
                 }
-                if (lane < kBlocks)
-                    cp_async16(dst + S::kKs + 16 * lane, page + lay.k_scales() + at * kBlocks + 16 * lane);
-                else if (lane < 2 * kBlocks)
-                    cp_async16(dst + S::kVs + 16 * (lane - kBlocks),
-                               page + lay.v_scales() + at * kBlocks + 16 * (lane - kBlocks));
-            } else if (lane == 0) {
-                report_index();
             }
         }
         cp_async_commit();
+        ahead += 128;
     };
-    {
-        int32_t pg[kStages - 1];
+    int pg0 = page_of(ahead), pg1 = page_of(ahead + 16);
 #pragma unroll
-        for (int i = 0; i < kStages - 1; ++i) pg[i] = page_of(i);
-#pragma unroll
-        for (int i = 0; i < kStages - 1; ++i) fetch(i, pg[i]);
+    for (unsigned i = 0; i < kStages - 1; ++i) {
+        const int n0 = page_of(ahead + 128), n1 = page_of(ahead + 144);
+        fetch(i, pg0, pg1);
+        pg0 = n0, pg1 = n1;
     }
-    int32_t next_page = page_of(kStages - 1);
 
     for (int r = warp; r < kRows; r += 4) {
         const bool real = r < nrows;
@@ -235,11 +301,11 @@ __global__ void __launch_bounds__(kFewThreads) attend_few_kernel(const __grid_co
         const float mul = query_multiplier(E);
 #pragma unroll
         for (int i = 0; i < kBlocks; ++i)
-            q_s[r][32 * i + lane] = __float2half_rn(warp_fwht32(x[i] * mul, lane) * kHadamardNorm);
+            sm.q[r][32 * i + lane] = __float2half_rn(warp_fwht32(x[i] * mul, lane) * kHadamardNorm);
         if (lane == 0) {
-            factor_s[r] = score_factor(p.scale_log2, E);
-            lo_s[r] = first_key(p, s.pos0 + qi);
-            hi_s[r] = real ? s.pos0 + qi : -1;
+            sm.factor[r] = score_factor(p.scale_log2, E);
+            sm.lo[r] = first_key(p, s.pos0 + qi);
+            sm.hi[r] = real ? s.pos0 + qi : -1;
         }
     }
     __syncthreads();
@@ -248,194 +314,237 @@ __global__ void __launch_bounds__(kFewThreads) attend_few_kernel(const __grid_co
     uint4 qf[kBlocks];
     if constexpr (NT == 1) {
 #pragma unroll
-        for (int i = 0; i < kBlocks; ++i) qf[i] = *reinterpret_cast<const uint4*>(&q_s[g][32 * i + 8 * c]);
+        for (int i = 0; i < kBlocks; ++i) qf[i] = *reinterpret_cast<const uint4*>(&sm.q[g][32 * i + 8 * c]);
     }
     float f[NT][2], ref[NT][2], bound[NT][2], sum[NT][2], o[NT][2 * kBlocks][4];
-    int vref = 0;  // the largest V scale met, to which the sums are relative
+    const int vp = D == 128 ? lane >> 2 : (lane >> 1) & 7, vb = lane & (kBlocks - 1);
+    int vref = 0;  // above the largest V scale met, which the sums are relative to
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            f[n][e] = factor_s[8 * n + 2 * c + e];
+            f[n][e] = sm.factor[8 * n + 2 * c + e];
             ref[n][e] = 0.0f, bound[n][e] = -INFINITY, sum[n][e] = 0.0f;
         }
 #pragma unroll
         for (int i = 0; i < 2 * kBlocks; ++i) o[n][i][0] = o[n][i][1] = o[n][i][2] = o[n][i][3] = 0.0f;
     }
 
-    for (int i = 0; i < count; ++i) {
+    unsigned stage = 0;
+    int base = (begin + warp) * 32;
+    for (int i = 0; i < count; ++i, base += 128) {
         cp_async_wait<kStages - 2>();
         __syncwarp();
-        fetch(i + kStages - 1, next_page);
-        next_page = page_of(i + kStages);
-        const int stage = i % kStages;
-        const uint8_t* st = ring + stage * S::kBytes;
-        const int base = (part.begin + warp + 4 * i) * 16;
-        const bool gone = (bad >> stage) & 1u;
-
-        float sc[NT][4];
-#pragma unroll
-        for (int n = 0; n < NT; ++n) sc[n][0] = sc[n][1] = sc[n][2] = sc[n][3] = 0.0f;
-        uint32_t k0[kBlocks], k1[kBlocks], ks0, ks1;
-        if constexpr (D == 128) {
-            const uint4 a = *reinterpret_cast<const uint4*>(st + g * 64 + c * 16);
-            const uint4 z = *reinterpret_cast<const uint4*>(st + (g + 8) * 64 + c * 16);
-            k0[0] = a.x, k0[1] = a.y, k0[2] = a.z, k0[3] = a.w;
-            k1[0] = z.x, k1[1] = z.y, k1[2] = z.z, k1[3] = z.w;
-            ks0 = *reinterpret_cast<const uint32_t*>(st + S::kKs + 4 * g);
-            ks1 = *reinterpret_cast<const uint32_t*>(st + S::kKs + 4 * (g + 8));
-        } else {
-            const uint2 a = *reinterpret_cast<const uint2*>(st + g * 32 + c * 8);
-            const uint2 z = *reinterpret_cast<const uint2*>(st + (g + 8) * 32 + c * 8);
-            k0[0] = a.x, k0[1] = a.y, k1[0] = z.x, k1[1] = z.y;
-            ks0 = *reinterpret_cast<const uint16_t*>(st + S::kKs + 2 * g);
-            ks1 = *reinterpret_cast<const uint16_t*>(st + S::kKs + 2 * (g + 8));
-        }
-#pragma unroll
-        for (int j = 0; j < kBlocks; ++j) {
-            const uint32_t a[4] = {e2m1x2_to_f16x2<0>(k0[j]), e2m1x2_to_f16x2<1>(k0[j]), e2m1x2_to_f16x2<2>(k0[j]),
-                                   e2m1x2_to_f16x2<3>(k0[j])};
-            const uint32_t z[4] = {e2m1x2_to_f16x2<0>(k1[j]), e2m1x2_to_f16x2<1>(k1[j]), e2m1x2_to_f16x2<2>(k1[j]),
-                                   e2m1x2_to_f16x2<3>(k1[j])};
-            // 2^(e - 127) of the two tokens' blocks (e = 0, below the smallest normal, counts as 0)
-            const float x0 = __uint_as_float(((ks0 >> (8 * j)) & 0xFFu) << 23);
-            const float x1 = __uint_as_float(((ks1 >> (8 * j)) & 0xFFu) << 23);
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                uint4 q;
-                if constexpr (NT == 1)
-                    q = qf[j];
-                else
-                    q = *reinterpret_cast<const uint4*>(&q_s[8 * n + g][32 * j + 8 * c]);
-                float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                mma_f16_16x8x16(acc, a[0], z[0], a[1], z[1], q.x, q.y);
-                mma_f16_16x8x16(acc, a[2], z[2], a[3], z[3], q.z, q.w);
-                sc[n][0] += acc[0] * x0, sc[n][1] += acc[1] * x0;
-                sc[n][2] += acc[2] * x1, sc[n][3] += acc[3] * x1;
-            }
-        }
-
-        // V scales of tokens 2c, 2c + 1 and 2c + 8, 2c + 9, two tokens' bytes of block j in 16-bit lanes
-        uint32_t vs0[kBlocks], vs1[kBlocks];
+        const unsigned gone2 = gone_bits >> (2 * stage);
         {
-            uint32_t w[4];
+            const int n0 = page_of(ahead + 128), n1 = page_of(ahead + 144);
+            fetch(stage == 0 ? kStages - 1 : stage - 1, pg0, pg1);
+            pg0 = n0, pg1 = n1;
+        }
+        const uint8_t* st0 = ring + stage * 2 * S::kBytes;
+        stage = stage == kStages - 1 ? 0 : stage + 1;
+
+        // The scales are widened once for the warp, two (D = 64: one) K values and one pair of V values a lane
+        // and strip: block vb of tokens 2 vp, 2 vp + 1.  (e = 0, below the smallest normal, counts as 0.)
+        int ve[2][2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const uint8_t* st = st0 + u * S::kBytes;
+            ve[u][0] = st[S::kVs + 2 * kBlocks * vp + vb], ve[u][1] = st[S::kVs + 2 * kBlocks * vp + kBlocks + vb];
+            float* ks = &sm.kscale[warp][u][0][0];
             if constexpr (D == 128) {
-                const uint2 lo = *reinterpret_cast<const uint2*>(st + S::kVs + 8 * c);
-                const uint2 hi = *reinterpret_cast<const uint2*>(st + S::kVs + 8 * c + 32);
-                w[0] = lo.x, w[1] = lo.y, w[2] = hi.x, w[3] = hi.y;
+                const uint32_t w = *reinterpret_cast<const uint16_t*>(st + S::kKs + 2 * lane);
+                *reinterpret_cast<float2*>(ks + 2 * lane) =
+                    make_float2(__uint_as_float((w & 0xFFu) << 23), __uint_as_float((w << 15) & 0x7F800000u));
             } else {
-                const uint32_t lo = *reinterpret_cast<const uint32_t*>(st + S::kVs + 4 * c);
-                const uint32_t hi = *reinterpret_cast<const uint32_t*>(st + S::kVs + 4 * c + 16);
-                w[0] = lo & 0xFFFFu, w[1] = lo >> 16, w[2] = hi & 0xFFFFu, w[3] = hi >> 16;
+                ks[lane] = __uint_as_float(static_cast<uint32_t>(st[S::kKs + lane]) << 23);
             }
-            if (gone || base < sp.last_lo || base + 15 > sp.first_hi) {  // a strip that some row's mask cuts
+        }
+        __syncwarp();
+
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
+        for (int half = 0; half < 2; half += kSub) {
+            float sc[kSub][NT][4];
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int lo = lo_s[8 * n + 2 * c + e], hi = gone ? -1 : hi_s[8 * n + 2 * c + e];
-                        const int t = base + g;
-                        if (t < lo || t > hi) sc[n][e] = -INFINITY;
-                        if (t + 8 < lo || t + 8 > hi) sc[n][2 + e] = -INFINITY;
+            for (int u = 0; u < kSub; ++u) {
+                const uint8_t* st = st0 + (half + u) * S::kBytes;
+                const float* ks = &sm.kscale[warp][half + u][0][0];
+#pragma unroll
+                for (int n = 0; n < NT; ++n) sc[u][n][0] = sc[u][n][1] = sc[u][n][2] = sc[u][n][3] = 0.0f;
+                uint32_t k0[kBlocks], k1[kBlocks];
+                float x0[kBlocks], x1[kBlocks];
+                if constexpr (D == 128) {
+                    const uint4 a = *reinterpret_cast<const uint4*>(st + g * 64 + c * 16);
+                    const uint4 z = *reinterpret_cast<const uint4*>(st + (g + 8) * 64 + c * 16);
+                    k0[0] = a.x, k0[1] = a.y, k0[2] = a.z, k0[3] = a.w;
+                    k1[0] = z.x, k1[1] = z.y, k1[2] = z.z, k1[3] = z.w;
+                    const float4 y = *reinterpret_cast<const float4*>(ks + 4 * g);
+                    const float4 v = *reinterpret_cast<const float4*>(ks + 4 * (g + 8));
+                    x0[0] = y.x, x0[1] = y.y, x0[2] = y.z, x0[3] = y.w;
+                    x1[0] = v.x, x1[1] = v.y, x1[2] = v.z, x1[3] = v.w;
+                } else {
+                    const uint2 a = *reinterpret_cast<const uint2*>(st + g * 32 + c * 8);
+                    const uint2 z = *reinterpret_cast<const uint2*>(st + (g + 8) * 32 + c * 8);
+                    k0[0] = a.x, k0[1] = a.y, k1[0] = z.x, k1[1] = z.y;
+                    const float2 y = *reinterpret_cast<const float2*>(ks + 2 * g);
+                    const float2 v = *reinterpret_cast<const float2*>(ks + 2 * (g + 8));
+                    x0[0] = y.x, x0[1] = y.y, x1[0] = v.x, x1[1] = v.y;
+                }
+#pragma unroll
+                for (int j = 0; j < kBlocks; ++j) {
+                    uint32_t a[4], z[4];
+                    e2m1x8_to_f16(k0[j], a);
+                    e2m1x8_to_f16(k1[j], z);
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        uint4 q;
+                        if constexpr (NT == 1)
+                            q = qf[j];
+                        else
+                            q = *reinterpret_cast<const uint4*>(&sm.q[8 * n + g][32 * j + 8 * c]);
+                        float acc[4];
+                        mma_f16_16x8x16_first(acc, a[0], z[0], a[1], z[1], q.x, q.y);
+                        mma_f16_16x8x16(acc, a[2], z[2], a[3], z[3], q.z, q.w);
+                        sc[u][n][0] += acc[0] * x0[j], sc[u][n][1] += acc[1] * x0[j];
+                        sc[u][n][2] += acc[2] * x1[j], sc[u][n][3] += acc[3] * x1[j];
                     }
                 }
-                // what lies there may be anything: no scale of a token that no row sees is used
+            }
+
+            const int from = base + 16 * half;
+            if (((gone2 >> half) & ((1u << kSub) - 1)) || from < sp.last_lo || from + 16 * kSub - 1 > sp.first_hi) {
+                // strips that some row's mask cuts
 #pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    const int t = base + 2 * c + (u & 1) + 4 * (u & 2);
-                    if (gone || t < sp.first_lo || t > sp.last_hi) w[u] = 0;
+                for (int u = 0; u < kSub; ++u) {
+                    const bool gone = (gone2 >> (half + u)) & 1u;
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int lo = sm.lo[8 * n + 2 * c + e], hi = gone ? -1 : sm.hi[8 * n + 2 * c + e];
+                            const int t = from + 16 * u + g;
+                            if (t < lo || t > hi) sc[u][n][e] = -INFINITY;
+                            if (t + 8 < lo || t + 8 > hi) sc[u][n][2 + e] = -INFINITY;
+                        }
+                    }
+                    // what lies there may be anything: no scale of a token that no row sees is used
+                    const int t = from + 16 * u + 2 * vp;
+                    if (gone || t < sp.first_lo || t > sp.last_hi) ve[half + u][0] = 0;
+                    if (gone || t + 1 < sp.first_lo || t + 1 > sp.last_hi) ve[half + u][1] = 0;
                 }
             }
-#pragma unroll
-            for (int j = 0; j < kBlocks; ++j) {
-                const uint32_t sel = j | j << 4 | (4 + j) << 8 | (4 + j) << 12;
-                vs0[j] = __byte_perm(w[0], w[1], sel) & 0x00FF00FFu;
-                vs1[j] = __byte_perm(w[2], w[3], sel) & 0x00FF00FFu;
-            }
-        }
-        uint32_t vtop = __vmaxs2(vs0[0], vs1[0]);
-#pragma unroll
-        for (int j = 1; j < kBlocks; ++j) vtop = __vimax3_s16x2(vtop, vs0[j], vs1[j]);
-        const int vmax = max(static_cast<int>(vtop & 0xFFFFu), static_cast<int>(vtop >> 16));
+            int vmax = max(ve[half][0], ve[half][1]);
+            if constexpr (kSub == 2) vmax = max(vmax, max(ve[1][0], ve[1][1]));
 
-        bool grow = vmax > vref;
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) grow |= fmaxf(sc[n][e], sc[n][2 + e]) * f[n][e] > bound[n][e];
-        if (__any_sync(0xFFFFFFFFu, grow)) {
-            const int nv = max(vref, static_cast<int>(__reduce_max_sync(0xFFFFFFFFu, static_cast<unsigned>(vmax))));
-            const float vf = nv - vref < 127 ? __uint_as_float(static_cast<uint32_t>(127 - (nv - vref)) << 23) : 0.0f;
-            vref = nv;
+            float top[NT][2];
+            bool grow = vmax > vref;
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    float m = fmaxf(sc[n][e], sc[n][2 + e]) * f[n][e];
-#pragma unroll
-                    for (int x = 4; x < 32; x <<= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, x));
-                    float scale = vf;
-                    if (m > bound[n][e] - kSlack) {  // false while a row has seen nothing
-                        const float old = ref[n][e];
-                        ref[n][e] = m - kLift;
-                        const float shift = bound[n][e] == -INFINITY ? 0.0f : exp2_approx(old - ref[n][e]);
-                        bound[n][e] = m + kSlack;
-                        sum[n][e] *= shift;
-                        scale *= shift;
-                    }
-#pragma unroll
-                    for (int x = 0; x < 2 * kBlocks; ++x) o[n][x][e] *= scale, o[n][x][2 + e] *= scale;
+                    top[n][e] = fmaxf(sc[0][n][e], sc[0][n][2 + e]);
+                    if constexpr (kSub == 2) top[n][e] = fmaxf(top[n][e], fmaxf(sc[1][n][e], sc[1][n][2 + e]));
+                    top[n][e] *= f[n][e];
+                    grow |= top[n][e] > bound[n][e];
                 }
             }
-        }
-
-        // softmax weights, transposed into fragments: tokens 2c, 2c + 1 (2c + 8, 2c + 9) of row g
-        uint32_t pt0[NT], pt1[NT];
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            float e0 = exp2_approx(fmaf(sc[n][0], f[n][0], -ref[n][0])), e1 = exp2_approx(fmaf(sc[n][1], f[n][1], -ref[n][1]));
-            float e2 = exp2_approx(fmaf(sc[n][2], f[n][0], -ref[n][0])), e3 = exp2_approx(fmaf(sc[n][3], f[n][1], -ref[n][1]));
-            sum[n][0] += e0 + e2, sum[n][1] += e1 + e3;
-            const __half2 a = __floats2half2_rn(e0, e1), z = __floats2half2_rn(e2, e3);
-            pt0[n] = movmatrix_trans(*reinterpret_cast<const uint32_t*>(&a));
-            pt1[n] = movmatrix_trans(*reinterpret_cast<const uint32_t*>(&z));
-        }
-
-        uint32_t va[4], vz[4];  // pairs c and c + 4: (first token: blocks 01, 23), (second token: 01, 23)
-        if constexpr (D == 128) {
-            const uint4 a = *reinterpret_cast<const uint4*>(st + S::kV + 16 * S::v_piece(c, g));
-            const uint4 z = *reinterpret_cast<const uint4*>(st + S::kV + 16 * S::v_piece(c + 4, g));
-            va[0] = a.x, va[1] = a.y, va[2] = a.z, va[3] = a.w;
-            vz[0] = z.x, vz[1] = z.y, vz[2] = z.z, vz[3] = z.w;
-        } else {
-            const uint2 a = *reinterpret_cast<const uint2*>(st + S::kV + 16 * S::v_piece(c, g >> 1) + 8 * (g & 1));
-            const uint2 z = *reinterpret_cast<const uint2*>(st + S::kV + 16 * S::v_piece(c + 4, g >> 1) + 8 * (g & 1));
-            va[0] = a.x, va[1] = a.y, vz[0] = z.x, vz[1] = z.y;
-        }
-        const uint32_t k2 = static_cast<uint32_t>((15 - vref) & 0xFFFF) * 0x00010001u;
-#pragma unroll
-        for (int h = 0; h < kBlocks / 2; ++h) {
-            // bytes whose nibbles are one element of the two tokens: elements 0, 2 and 1, 3 of two blocks
-            const uint32_t a0 = va[h], a1 = va[kBlocks / 2 + h], z0 = vz[h], z1 = vz[kBlocks / 2 + h];
-            const uint32_t ae = (a0 & 0x0F0F0F0Fu) | ((a1 << 4) & 0xF0F0F0F0u), ao = ((a0 >> 4) & 0x0F0F0F0Fu) | (a1 & 0xF0F0F0F0u);
-            const uint32_t ze = (z0 & 0x0F0F0F0Fu) | ((z1 << 4) & 0xF0F0F0F0u), zo = ((z0 >> 4) & 0x0F0F0F0Fu) | (z1 & 0xF0F0F0F0u);
-            const uint32_t ea[4] = {e2m1x2_to_f16x2<0>(ae), e2m1x2_to_f16x2<1>(ae), e2m1x2_to_f16x2<2>(ae), e2m1x2_to_f16x2<3>(ae)};
-            const uint32_t oa[4] = {e2m1x2_to_f16x2<0>(ao), e2m1x2_to_f16x2<1>(ao), e2m1x2_to_f16x2<2>(ao), e2m1x2_to_f16x2<3>(ao)};
-            const uint32_t ez[4] = {e2m1x2_to_f16x2<0>(ze), e2m1x2_to_f16x2<1>(ze), e2m1x2_to_f16x2<2>(ze), e2m1x2_to_f16x2<3>(ze)};
-            const uint32_t oz[4] = {e2m1x2_to_f16x2<0>(zo), e2m1x2_to_f16x2<1>(zo), e2m1x2_to_f16x2<2>(zo), e2m1x2_to_f16x2<3>(zo)};
-#pragma unroll
-            for (int y = 0; y < 2; ++y) {
-                const int j = 2 * h + y;
-                // f16 2^(e - vref) of two tokens: exponent field e - vref + 15, 0 below it
-                const uint32_t x0 = __viaddmin_s16x2_relu(vs0[j], k2, 0x000F000Fu) << 10;
-                const uint32_t x1 = __viaddmin_s16x2_relu(vs1[j], k2, 0x000F000Fu) << 10;
+            if (__any_sync(0xFFFFFFFFu, grow)) {
+                float vf = 1.0f;
+                const int nv = static_cast<int>(__reduce_max_sync(0xFFFFFFFFu, static_cast<unsigned>(vmax)));
+                if (nv > vref) {  // with room for three doublings before the next time
+                    const int to = min(nv + 3, 254);
+                    vf = to - vref < 127 ? __uint_as_float(static_cast<uint32_t>(127 - (to - vref)) << 23) : 0.0f;
+                    vref = to;
+                }
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
-                    const __half2 b0 = __hmul2(*reinterpret_cast<const __half2*>(&pt0[n]), *reinterpret_cast<const __half2*>(&x0));
-                    const __half2 b1 = __hmul2(*reinterpret_cast<const __half2*>(&pt1[n]), *reinterpret_cast<const __half2*>(&x1));
-                    const uint32_t u0 = *reinterpret_cast<const uint32_t*>(&b0), u1 = *reinterpret_cast<const uint32_t*>(&b1);
-                    mma_f16_16x8x16(o[n][2 * j], ea[2 * y], oa[2 * y], ez[2 * y], oz[2 * y], u0, u1);
-                    mma_f16_16x8x16(o[n][2 * j + 1], ea[2 * y + 1], oa[2 * y + 1], ez[2 * y + 1], oz[2 * y + 1], u0, u1);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float m = top[n][e];
+#pragma unroll
+                        for (int x = 4; x < 32; x <<= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, x));
+                        float scale = vf;
+                        if (m > bound[n][e] - kSlack) {  // false while a row has seen nothing
+                            const float old = ref[n][e];
+                            ref[n][e] = m - kLift;
+                            const float shift = bound[n][e] == -INFINITY ? 0.0f : exp2_approx(old - ref[n][e]);
+                            bound[n][e] = m + kSlack;
+                            sum[n][e] *= shift;
+                            scale *= shift;
+                        }
+#pragma unroll
+                        for (int x = 0; x < 2 * kBlocks; ++x) o[n][x][e] *= scale, o[n][x][2 + e] *= scale;
+                    }
+                }
+            }
+
+            // exponent field e - vref + 15 of two tokens, 0 below it
+            const uint32_t k2 = static_cast<uint32_t>((15 - vref) & 0xFFFF) * 0x00010001u;
+#pragma unroll
+            for (int u = 0; u < kSub; ++u)
+                sm.vscale[warp][half + u][vp][vb] =
+                    __viaddmin_s16x2_relu(static_cast<uint32_t>(ve[half + u][0] | ve[half + u][1] << 16), k2, 0x000F000Fu) << 10;
+            __syncwarp();
+
+#pragma unroll
+            for (int u = 0; u < kSub; ++u) {
+                const uint8_t* st = st0 + (half + u) * S::kBytes;
+                // softmax weights, transposed into fragments: tokens 2c, 2c + 1 (2c + 8, 2c + 9) of row g
+                uint32_t pt0[NT], pt1[NT];
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    const float e0 = exp2_approx(fmaf(sc[u][n][0], f[n][0], -ref[n][0]));
+                    const float e1 = exp2_approx(fmaf(sc[u][n][1], f[n][1], -ref[n][1]));
+                    const float e2 = exp2_approx(fmaf(sc[u][n][2], f[n][0], -ref[n][0]));
+                    const float e3 = exp2_approx(fmaf(sc[u][n][3], f[n][1], -ref[n][1]));
+                    sum[n][0] += e0 + e2, sum[n][1] += e1 + e3;
+                    const __half2 a = __floats2half2_rn(e0, e1), z = __floats2half2_rn(e2, e3);
+                    pt0[n] = movmatrix_trans(*reinterpret_cast<const uint32_t*>(&a));
+                    pt1[n] = movmatrix_trans(*reinterpret_cast<const uint32_t*>(&z));
+                }
+                uint32_t va[4], vz[4];  // pairs c and c + 4: (first token: blocks 01, 23), (second token: 01, 23)
+                uint32_t vx0[kBlocks], vx1[kBlocks];
+                const uint32_t* vs = &sm.vscale[warp][half + u][0][0];
+                if constexpr (D == 128) {
+                    const uint4 a = *reinterpret_cast<const uint4*>(st + S::kV + 16 * S::v_piece(c, g));
+                    const uint4 z = *reinterpret_cast<const uint4*>(st + S::kV + 16 * S::v_piece(c + 4, g));
+                    va[0] = a.x, va[1] = a.y, va[2] = a.z, va[3] = a.w;
+                    vz[0] = z.x, vz[1] = z.y, vz[2] = z.z, vz[3] = z.w;
+                    const uint4 y = *reinterpret_cast<const uint4*>(vs + 4 * c);
+                    const uint4 w = *reinterpret_cast<const uint4*>(vs + 4 * (c + 4));
+                    vx0[0] = y.x, vx0[1] = y.y, vx0[2] = y.z, vx0[3] = y.w;
+                    vx1[0] = w.x, vx1[1] = w.y, vx1[2] = w.z, vx1[3] = w.w;
+                } else {
+                    const uint2 a = *reinterpret_cast<const uint2*>(st + S::kV + 16 * S::v_piece(c, g >> 1) + 8 * (g & 1));
+                    const uint2 z = *reinterpret_cast<const uint2*>(st + S::kV + 16 * S::v_piece(c + 4, g >> 1) + 8 * (g & 1));
+                    va[0] = a.x, va[1] = a.y, vz[0] = z.x, vz[1] = z.y;
+                    const uint2 y = *reinterpret_cast<const uint2*>(vs + 2 * c);
+                    const uint2 w = *reinterpret_cast<const uint2*>(vs + 2 * (c + 4));
+                    vx0[0] = y.x, vx0[1] = y.y, vx1[0] = w.x, vx1[1] = w.y;
+                }
+#pragma unroll
+                for (int h = 0; h < kBlocks / 2; ++h) {
+                    // bytes whose nibbles are one element of the two tokens: elements 0, 2 and 1, 3 of two blocks
+                    const uint32_t a0 = va[h], a1 = va[kBlocks / 2 + h], z0 = vz[h], z1 = vz[kBlocks / 2 + h];
+                    const uint32_t ae = (a0 & 0x0F0F0F0Fu) | ((a1 << 4) & 0xF0F0F0F0u);
+                    const uint32_t ao = ((a0 >> 4) & 0x0F0F0F0Fu) | (a1 & 0xF0F0F0F0u);
+                    const uint32_t ze = (z0 & 0x0F0F0F0Fu) | ((z1 << 4) & 0xF0F0F0F0u);
+                    const uint32_t zo = ((z0 >> 4) & 0x0F0F0F0Fu) | (z1 & 0xF0F0F0F0u);
+                    uint32_t ea[4], oa[4], ez[4], oz[4];
+                    e2m1x8_to_f16(ae, ea), e2m1x8_to_f16(ao, oa);
+                    e2m1x8_to_f16(ze, ez), e2m1x8_to_f16(zo, oz);
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+                        const int j = 2 * h + y;
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) {
+                            const __half2 b0 = __hmul2(*reinterpret_cast<const __half2*>(&pt0[n]), *reinterpret_cast<const __half2*>(&vx0[j]));
+                            const __half2 b1 = __hmul2(*reinterpret_cast<const __half2*>(&pt1[n]), *reinterpret_cast<const __half2*>(&vx1[j]));
+                            const uint32_t u0 = *reinterpret_cast<const uint32_t*>(&b0), u1 = *reinterpret_cast<const uint32_t*>(&b1);
+                            mma_f16_16x8x16(o[n][2 * j], ea[2 * y], oa[2 * y], ez[2 * y], oz[2 * y], u0, u1);
+                            mma_f16_16x8x16(o[n][2 * j + 1], ea[2 * y + 1], oa[2 * y + 1], ez[2 * y + 1], oz[2 * y + 1], u0, u1);
+                        }
+                    }
                 }
             }
         }
@@ -443,9 +552,7 @@ __global__ void __launch_bounds__(kFewThreads) attend_few_kernel(const __grid_co
     cp_async_wait<0>();
 
     // join the warps, one n-tile (8 rows) at a time: warp w's sums of row r at joined[w][r][..]
-    float* joined = reinterpret_cast<float*>(dynamic_smem);
-    const int64_t units = static_cast<int64_t>(p.B) * p.Hk * p.row_tiles;
-    const int64_t unit = bh * p.row_tiles + rt;
+    float* joined = reinterpret_cast<float*>(sm.ring);
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
         if (8 * n >= nrows) break;
@@ -455,14 +562,14 @@ __global__ void __launch_bounds__(kFewThreads) attend_few_kernel(const __grid_co
             float t = sum[n][e];
 #pragma unroll
             for (int x = 4; x < 32; x <<= 1) t += __shfl_xor_sync(0xFFFFFFFFu, t, x);
-            if (g == 0) ml_s[warp][2 * c + e] = make_float2(bound[n][e] == -INFINITY ? -INFINITY : ref[n][e], t);
+            if (g == 0) sm.ml[warp][2 * c + e] = make_float2(bound[n][e] == -INFINITY ? -INFINITY : ref[n][e], t);
 #pragma unroll
             for (int j = 0; j < 2 * kBlocks; ++j) {
                 float* row = joined + (warp * 8 + 2 * c + e) * D + 16 * j + 4 * g - (j & 1) * 14;
-                row[0] = o[n][j][e], row[1] = o[n][j][2 + e];
+                *reinterpret_cast<float2*>(row) = make_float2(o[n][j][e], o[n][j][2 + e]);
             }
         }
-        if (lane == 0) vref_s[warp] = vref ? __uint_as_float(static_cast<uint32_t>(vref) << 23) : 0.0f;
+        if (lane == 0) sm.vref[warp] = __uint_as_float(static_cast<uint32_t>(vref) << 23);
         __syncthreads();
         constexpr int kAtOnce = kFewThreads / D;
         const int d = threadIdx.x % D;
@@ -472,18 +579,18 @@ __global__ void __launch_bounds__(kFewThreads) attend_few_kernel(const __grid_co
             if (8 * n + r >= nrows) continue;
             float m = -INFINITY, total = 0.0f, x = 0.0f, w[4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) m = fmaxf(m, ml_s[k][r].x);
+            for (int k = 0; k < 4; ++k) m = fmaxf(m, sm.ml[k][r].x);
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                w[k] = ml_s[k][r].x == -INFINITY ? 0.0f : exp2_approx(ml_s[k][r].x - m);
-                total += w[k] * ml_s[k][r].y;
+                w[k] = sm.ml[k][r].x == -INFINITY ? 0.0f : exp2_approx(sm.ml[k][r].x - m);
+                total += w[k] * sm.ml[k][r].y;
             }
             const float inv = total > 0.0f ? 1.0f / total : total == 0.0f ? 0.0f : total;
 #pragma unroll
             for (int k = 0; k < 4; ++k)  // divided first: the sums times a large scale might not fit
-                if (w[k] != 0.0f) x += joined[(k * 8 + r) * D + d] * (w[k] * inv) * vref_s[k];
-            if (p.splits > 1) {
-                const int64_t at = (split * units + unit) * p.tile_rows + 8 * n + r;
+                if (w[k] != 0.0f) x += joined[(k * 8 + r) * D + d] * (w[k] * inv) * sm.vref[k];
+            if (slot >= 0) {
+                const int64_t at = slot * p.tile_rows + 8 * n + r;
                 p.part_o[at * D + d] = x;
                 if (d == 0) p.part_ml[at] = make_float2(m, total);
             } else {
@@ -495,9 +602,60 @@ __global__ void __launch_bounds__(kFewThreads) attend_few_kernel(const __grid_co
             }
         }
     }
+    __syncthreads();
 }
 
-// Joins the parts of a row: one warp per (sequence, query, head).
+template <int D, int NT>
+__global__ void __launch_bounds__(kFewThreads, few_resident(NT)) attend_few_kernel(const __grid_constant__ AttendParams p) {
+    extern __shared__ uint4 dynamic_smem[];
+    FewShared<D, NT>& sm = *reinterpret_cast<FewShared<D, NT>*>(dynamic_smem);
+    constexpr int kRows = 8 * NT;
+    griddep_launch_dependents();
+    griddep_wait();
+    if (!p.ctas) {  // one unit
+        const int64_t block = blockIdx.x, bh = block / p.row_tiles;
+        const int b = static_cast<int>(bh / p.Hk);
+        const Sequence s = sequence_of(p, b);
+        const int r0 = static_cast<int>(block % p.row_tiles) * kRows;
+        const int nrows = min(kRows, s.nq * p.G - r0);
+        if (nrows <= 0) return;
+        const Span sp = span_of(p, s, r0, nrows);
+        const int begin = sp.first_lo >> kFewShift;
+        few_unit<D, NT>(p, sm, s, b, static_cast<int>(bh % p.Hk), r0, nrows, sp, begin, begin + blocks_of(sp, kFewShift), -1);
+        return;
+    }
+    Cut cut = cut_of(p, kFewShift, sm.scan, &sm.first_seq, &sm.first_pos);
+    while (cut.pos < cut.end) {
+        const Sequence s = sequence_of(p, cut.b);
+        const int rows = s.nq * p.G;
+        const int64_t per_head = sequence_blocks(p, s, kFewShift);
+        int64_t off = cut.pos - cut.seq_pos;
+        if (per_head == 0 || off >= per_head * p.Hk) {
+            cut.seq_pos += per_head * p.Hk;
+            ++cut.b;
+            continue;
+        }
+        const int kvh = static_cast<int>(off / per_head);
+        off -= kvh * per_head;
+        int r0 = 0, n = 0;
+        Span sp = {};
+        for (;; r0 += kRows) {
+            sp = span_of(p, s, r0, min(kRows, rows - r0));
+            n = blocks_of(sp, kFewShift);
+            if (off < n) break;
+            off -= n;
+        }
+        const int from = static_cast<int>(off), to = static_cast<int>(min(static_cast<int64_t>(n), off + cut.end - cut.pos));
+        const bool whole = from == 0 && to == n;
+        const int64_t slot = whole ? -1 : 2 * static_cast<int64_t>(blockIdx.x) + (from == 0 ? 1 : 0);
+        const int begin = sp.first_lo >> kFewShift;
+        few_unit<D, NT>(p, sm, s, cut.b, kvh, r0, min(kRows, rows - r0), sp, begin + from, begin + to, slot);
+        cut.pos += to - from;
+    }
+}
+
+// Joins the parts of a row: one warp per (sequence, query, head).  Rows that one CTA wrote are left alone,
+// rows that see nothing get their zeros here.
 template <int D>
 __global__ void __launch_bounds__(128) attend_join_kernel(const __grid_constant__ AttendParams p, int shift) {
     constexpr int kElems = D / 32;  // of a lane, neighbours
@@ -509,26 +667,47 @@ __global__ void __launch_bounds__(128) attend_join_kernel(const __grid_constant_
     const int h = static_cast<int>(item - query * p.Hq);
     const int b = static_cast<int>(query / p.max_q), qi = static_cast<int>(query % p.max_q);
     if (b >= p.B) return;
+    int64_t before = 0, total_blocks = 0;
+    for (int x = lane; x < p.B; x += 32) {
+        const int64_t n = sequence_blocks(p, sequence_of(p, x), shift) * p.Hk;
+        total_blocks += n;
+        if (x < b) before += n;
+    }
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) {
+        total_blocks += __shfl_xor_sync(0xFFFFFFFFu, total_blocks, x);
+        before += __shfl_xor_sync(0xFFFFFFFFu, before, x);
+    }
     const Sequence s = sequence_of(p, b);
     if (qi >= s.nq) return;
-    const int kvh = h / p.G, r = qi * p.G + h - kvh * p.G;
-    const int rt = r / p.tile_rows, r0 = rt * p.tile_rows;
-    const Part part = part_of(p, span_of(p, s, r0, min(p.tile_rows, s.nq * p.G - r0)), shift, 0);
-    const int64_t stride = static_cast<int64_t>(p.B) * p.Hk * p.row_tiles * p.tile_rows;
-    const int64_t at = ((static_cast<int64_t>(b) * p.Hk + kvh) * p.row_tiles + rt) * p.tile_rows + (r - r0);
+    const int kvh = h / p.G, r = qi * p.G + h - kvh * p.G, rows = s.nq * p.G;
+    int64_t u0 = before + kvh * sequence_blocks(p, s, shift);
+    int r0 = 0, n = blocks_of(span_of(p, s, 0, min(p.tile_rows, rows)), shift);
+    while (r0 + p.tile_rows <= r) {
+        u0 += n;
+        r0 += p.tile_rows;
+        n = blocks_of(span_of(p, s, r0, min(p.tile_rows, rows - r0)), shift);
+    }
+    const int64_t len = cut_length(p, total_blocks, shift);
+    const int64_t c0 = u0 / len, c1 = n ? (u0 + n - 1) / len : c0 - 1;  // the CTAs that hold parts
+    if (c0 == c1) return;
+    // the first part is what its CTA's range ends in (slot 1), the others are what theirs begin with (slot 0)
+    const int64_t stride = 2 * p.tile_rows;
+    const int64_t at = c0 * stride + r - r0;
+    auto place = [&](int64_t k) { return at + k * stride + (k == 0 ? p.tile_rows : 0); };
+    const int parts = static_cast<int>(c1 - c0 + 1);
     float m = -INFINITY;
-    for (int k = lane; k < part.parts; k += 32) m = fmaxf(m, p.part_ml[k * stride + at].x);
+    for (int k = lane; k < parts; k += 32) m = fmaxf(m, p.part_ml[place(k)].x);
 #pragma unroll
     for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, x));
     float total = 0.0f, o[kElems] = {};
-    for (int k = 0; k < part.parts; ++k) {
-        const float2 ml = p.part_ml[k * stride + at];
+    for (int k = 0; k < parts; ++k) {
+        const float2 ml = p.part_ml[place(k)];
         const float w = ml.x == -INFINITY ? 0.0f : exp2_approx(ml.x - m) * ml.y;
-        if (w == 0.0f) continue;
+        const float* src = p.part_o + place(k) * D + kElems * lane;
         total += w;
-        const float* src = p.part_o + (k * stride + at) * D + kElems * lane;
 #pragma unroll
-        for (int j = 0; j < kElems; ++j) o[j] += w * src[j];
+        for (int j = 0; j < kElems; ++j) o[j] += w == 0.0f ? 0.0f : w * src[j];
     }
     const float inv = total > 0.0f ? kHadamardNorm / total : total == 0.0f ? 0.0f : total;
 #pragma unroll
@@ -558,9 +737,11 @@ __global__ void __launch_bounds__(128) attend_join_kernel(const __grid_constant_
 
 // ------------------------------------------------------------------------------------ host side
 
+constexpr int64_t kMaxKeys = int64_t{1} << 30;  // of a sequence: positions and block ends stay in 32 bits
+
 // How a call is split, from what the host knows (not the sequences' lengths).
 struct AttendPlan {
-    int tile_rows, row_tiles, splits;
+    int tile_rows, row_tiles, ctas;
     int64_t units;
     size_t bytes;
 };
@@ -570,34 +751,34 @@ static AttendPlan plan_attend(int64_t B, int Hq, int Hk, int D, int64_t max_q) {
     a.tile_rows = rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
     a.row_tiles = static_cast<int>((rows + a.tile_rows - 1) / a.tile_rows);
     a.units = B * Hk * a.row_tiles;
-    const int64_t wanted = static_cast<int64_t>(sm_count()) * 8;
-    a.splits = static_cast<int>(a.units >= wanted ? 1 : (wanted + a.units - 1) / a.units);
-    if (a.splits > 64) a.splits = 64;
-    const size_t rows_all = static_cast<size_t>(a.splits) * a.units * a.tile_rows;
-    a.bytes = a.splits > 1 ? rows_all * (static_cast<size_t>(D) * 4 + 8) : 0;
+    // cut while there are few units: many balance themselves, and need no joining
+    const int resident = sm_count() * few_resident(a.tile_rows / 8);
+    a.ctas = a.units >= 4 * resident ? 0 : resident;
+    a.bytes = static_cast<size_t>(a.ctas) * 2 * a.tile_rows * (static_cast<size_t>(D) * 4 + 8);
     a.bytes = (a.bytes + 255) / 256 * 256 + 256;
     return a;
 }
 
 template <int D, int NT>
 static int launch_few(const AttendParams& p, unsigned blocks, cudaStream_t stream) {
-    constexpr size_t kRing = 4 * kStages * Strip<D>::kBytes, kJoin = 4 * 8 * D * sizeof(float);
-    constexpr size_t kSmem = kRing > kJoin ? kRing : kJoin;
-    static_assert(kSmem + sizeof(__half) * 8 * NT * (D + 8) + 1024 <= 48 * 1024, "within the default limit");
+    constexpr size_t kSmem = sizeof(FewShared<D, NT>);
+    static_assert(few_resident(NT) * (kSmem + 1024) <= 228 * 1024, "shared memory of an SM");
+    if (cudaFuncSetAttribute(attend_few_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess)
+        return MACAQ_ECUDA;
     return launch_dependent_smem(attend_few_kernel<D, NT>, dim3(blocks), kFewThreads, kSmem, stream, p);
 }
 
 template <int D>
 static int launch_attend(const AttendParams& p, int64_t units, cudaStream_t stream) {
-    const int64_t blocks = units * p.splits;
+    const int64_t blocks = p.ctas ? p.ctas : units;
     const int64_t join = (static_cast<int64_t>(p.B) * p.max_q * p.Hq + 3) / 4;
     if (blocks > kMaxDim || join > kMaxDim) return MACAQ_ESHAPE;
     const auto n = static_cast<unsigned>(blocks);
     const int st = p.tile_rows == 8    ? launch_few<D, 1>(p, n, stream)
                    : p.tile_rows == 16 ? launch_few<D, 2>(p, n, stream)
                                        : launch_few<D, 4>(p, n, stream);
-    if (st != MACAQ_OK || p.splits == 1) return st;
-    return launch_dependent(attend_join_kernel<D>, dim3(static_cast<unsigned>(join)), 128, stream, p, 4);
+    if (st != MACAQ_OK || !p.ctas) return st;
+    return launch_dependent(attend_join_kernel<D>, dim3(static_cast<unsigned>(join)), 128, stream, p, kFewShift);
 }
 
 }  // namespace macaq
@@ -617,7 +798,7 @@ extern "C" int macaq_kv4_attention(const uint16_t* q, int64_t T, int64_t ldq, in
                                    void* workspace, size_t workspace_bytes, void* stream) {
     const size_t need = macaq_kv4_attention_workspace_bytes(T, B, Hq, Hk, head_dim, max_q);
     if (need == 0 || !page_size_ok(page_size) || num_pages < 1 || num_pages > kMaxDim || table_width < 0 ||
-        table_width > kMaxDim / page_size || ldq < static_cast<int64_t>(Hq) * head_dim || ldq > kMaxDim || ldq % 8 != 0 ||
+        table_width > kMaxKeys / page_size || ldq < static_cast<int64_t>(Hq) * head_dim || ldq > kMaxDim || ldq % 8 != 0 ||
         window < 0)
         return MACAQ_ESHAPE;
     if (!cu_q && (B != T || max_q != 1)) return MACAQ_ESHAPE;
@@ -635,12 +816,9 @@ extern "C" int macaq_kv4_attention(const uint16_t* q, int64_t T, int64_t ldq, in
     p.page_size = page_size, p.page_shift = __builtin_ctz(page_size), p.tables = tables, p.table_width = table_width;
     p.kv_lens = kv_lens, p.cu_q = cu_q, p.B = static_cast<int>(B), p.max_q = static_cast<int>(max_q);
     p.scale_log2 = scale * kLog2e, p.window = static_cast<int>(window < kMaxDim ? window : 0), p.out = out, p.lse = lse;
-    p.tile_rows = plan.tile_rows, p.row_tiles = plan.row_tiles, p.splits = plan.splits;
-    // no more parts than a full table gives
-    const int64_t most = (table_width * page_size + kMinKeys - 1) / kMinKeys;
-    if (p.splits > most) p.splits = static_cast<int>(most > 1 ? most : 1);
+    p.tile_rows = plan.tile_rows, p.row_tiles = plan.row_tiles, p.ctas = plan.ctas;
     p.part_ml = static_cast<float2*>(workspace);
-    p.part_o = reinterpret_cast<float*>(p.part_ml + static_cast<int64_t>(p.splits) * plan.units * p.tile_rows);
+    p.part_o = reinterpret_cast<float*>(p.part_ml + static_cast<int64_t>(p.ctas) * 2 * p.tile_rows);
     const auto s = static_cast<cudaStream_t>(stream);
     return head_dim == 64 ? launch_attend<64>(p, plan.units, s) : launch_attend<128>(p, plan.units, s);
 }

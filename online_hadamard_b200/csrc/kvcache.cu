@@ -407,7 +407,8 @@ __global__ void __launch_bounds__(kHeadThreads) heads_kernel(const __grid_consta
 
 // Eight E2M1 codes of a word (element j in nibble j) as floats.
 __device__ __forceinline__ void decode_e2m1x8(uint32_t w, float* f) {
-    const uint32_t h[4] = {e2m1x2_to_f16x2<0>(w), e2m1x2_to_f16x2<1>(w), e2m1x2_to_f16x2<2>(w), e2m1x2_to_f16x2<3>(w)};
+    uint32_t h[4];
+    e2m1x8_to_f16(w, h);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&h[j]));
