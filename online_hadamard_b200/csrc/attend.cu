@@ -191,13 +191,12 @@ constexpr int kFewThreads = 128;
 constexpr int kStages = 3;
 constexpr int kFewShift = 5;
 
+// A block of 32 tokens in shared memory: K codes, V codes, K scales, V scales.
 template <int D>
-struct Strip {
+struct TokenBlock {
     static constexpr int kBlocks = D / 32;
-    static constexpr int kV = 8 * D;         // K codes of 16 tokens come first
-    static constexpr int kKs = 16 * D;       // then V codes, then the scales
-    static constexpr int kVs = kKs + 16 * kBlocks;
-    static constexpr int kBytes = kVs + 16 * kBlocks;
+    static constexpr int kV = 16 * D, kKs = 32 * D, kVs = kKs + 32 * kBlocks, kBytes = kVs + 32 * kBlocks;
+    static constexpr int kStrip = 8 * D;  // codes of 16 tokens
     // 16-byte pieces of V lie swizzled, so that the fragment loads of 8 lanes meet 8 different banks
     __device__ static __forceinline__ int v_piece(int pair, int piece) {
         return D == 128 ? pair * 8 + (piece ^ ((pair & 3) * 2)) : pair * 4 + (piece ^ (((pair >> 1) & 1) * 2));
@@ -210,7 +209,7 @@ constexpr int few_resident(int NT) { return NT == 4 ? 2 : 3; }
 template <int D, int NT>
 struct FewShared {
     static constexpr int kBlocks = D / 32;
-    static constexpr size_t kRing = 4 * kStages * 2 * Strip<D>::kBytes, kJoin = 4 * 8 * D * sizeof(float);
+    static constexpr size_t kRing = 4 * kStages * TokenBlock<D>::kBytes, kJoin = 4 * 8 * D * sizeof(float);
     alignas(16) uint8_t ring[kRing > kJoin ? kRing : kJoin];  // in the end the warps' sums of 8 rows
     alignas(16) __half q[8 * NT][D + 8];
     alignas(16) float kscale[4][2][16][kBlocks];    // a warp's strips: 2^(e - 127) of K's blocks
@@ -228,61 +227,77 @@ struct FewShared {
 template <int D, int NT>
 __device__ __forceinline__ void few_unit(const AttendParams& p, FewShared<D, NT>& sm, const Sequence& s, int b, int kvh,
                                          int r0, int nrows, const Span& sp, int begin, int end, int64_t slot) {
-    using S = Strip<D>;
+    using S = TokenBlock<D>;
     constexpr int kBlocks = D / 32, kRows = 8 * NT;
     constexpr int kSub = NT == 4 ? 1 : 2;  // strips worked on together, as registers allow
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31, warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0);
     const int g = lane >> 2, c = lane & 3;
     const int count = max(0, (end - begin - warp + 3) >> 2);  // blocks of this warp
     const int32_t* table = p.tables + b * p.table_width;
-    uint8_t* ring = sm.ring + warp * kStages * 2 * S::kBytes;
-    unsigned gone_bits = 0;  // bits 2 stage + u: strips that were not copied
-    // what a lane copies: 16 bytes (D = 128: 32) of K and of V codes, and a piece of the scales
+    uint8_t* ring = sm.ring + warp * kStages * S::kBytes;
+    unsigned gone_bits = 0;  // bits 2 stage + u: strips (16 tokens) that were not copied
+    // what a lane copies: 16 bytes of every 512 of the codes, and a piece of the scales
     const PageLayout<D> lay{p.page_size};
     const uint8_t* head = p.cache + kvh * lay.bytes();
     const uint32_t page_stride = static_cast<uint32_t>(p.Hk * lay.bytes());
-    const int scale_at = lane < kBlocks ? lay.k_scales() + 16 * lane : lay.v_scales() + 16 * (lane - kBlocks);
     const uint32_t ring_at = smem_u32(ring) + 16 * lane;
     const uint32_t v_at = smem_u32(ring) + S::kV + 16 * S::v_piece(lane / (D / 16), lane % (D / 16));
-    int ahead = (begin + warp) * 32;                 // first token of the block to fetch next
+    const bool small_pages = p.page_size < 32;
+    const int scale_at = lane < 2 * kBlocks ? lay.k_scales() + 16 * lane : lay.v_scales() + 16 * (lane - 2 * kBlocks);
+    int ahead = (begin + warp) * 32;  // first token of the block to fetch next
     const int fetch_end = end * 32;
-    auto page_of = [&](int t) {  // -1: nothing of the strip is seen
-        return t < fetch_end && t <= sp.last_hi && t + 15 >= sp.first_lo ? table[t >> p.page_shift] : -1;
-    };
-    auto fetch = [&](unsigned stage, int pg0, int pg1) {
+    auto page_of = [&](int t) { return t < fetch_end ? table[t >> p.page_shift] : -1; };
+    auto fetch = [&](unsigned stage, int pg) {
         if (ahead < fetch_end) {
+            const uint32_t to = stage * S::kBytes;
+            gone_bits &= ~(3u << (2 * stage));
+            if (small_pages) {  // the block's strips lie in pages of their own
+#pragma unroll 1
+                for (int u = 0; u < 2; ++u) {
+                    const int t = ahead + 16 * u;
+                    const bool seen = t <= sp.last_hi && t + 15 >= sp.first_lo;
+                    const int pu = seen ? table[t >> 4] : -1;
+                    if (static_cast<unsigned>(pu) < static_cast<uint64_t>(p.num_pages)) {
+                        const uint8_t* page = head + static_cast<uint64_t>(static_cast<uint32_t>(pu)) * page_stride;
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const int pg = u ? pg1 : pg0, t = ahead + 16 * u;
-                const unsigned bit = 1u << (2 * stage + u);
-                gone_bits |= bit;
-                if (static_cast<unsigned>(pg) < static_cast<uint64_t>(p.num_pages)) {
-                    gone_bits &= ~bit;
-                    const int at = t & (p.page_size - 1);
-                    const uint8_t* page = head + static_cast<uint64_t>(static_cast<uint32_t>(pg)) * page_stride;
-                    const uint8_t* kc = page + (at * lay.kRow + 16 * lane);  // V's pair rows lie as far apart as two K rows
-                    const uint8_t* vc = kc + lay.v_codes();
-                    const uint32_t to = (2 * stage + u) * S::kBytes;
-#pragma unroll
-                    for (int x = 0; x < D / 64; ++x) {
-                        cp_async16(ring_at + to + 512 * x, kc + 512 * x);
-                        cp_async16(v_at + to + 512 * x, vc + 512 * x);
+                        for (int x = 0; x < D / 64; ++x) {
+                            const uint32_t at = to + u * S::kStrip + 512 * x;
+                            cp_async16(ring_at + at, page + 16 * lane + 512 * x);
+                            cp_async16(v_at + at, page + lay.v_codes() + 16 * lane + 512 * x);
+                        }
+                        if (lane < 2 * kBlocks)  // of K, then of V: the block's K scales lie between
+                            cp_async16(ring_at + to + S::kKs + 16 * kBlocks * u + (lane < kBlocks ? 0 : 16 * kBlocks),
+                                       page + lay.k_scales() + 16 * lane);
+                    } else {
+                        gone_bits |= 1u << (2 * stage + u);
+                        if (seen && lane == 0) report_index();
                     }
-                    if (lane < 2 * kBlocks) cp_async16(ring_at + to + S::kKs, page + (scale_at + at * kBlocks));
-                } else if (lane == 0 && t <= sp.last_hi && t + 15 >= sp.first_lo) {
-                    report_index();
                 }
+            } else if (static_cast<unsigned>(pg) < static_cast<uint64_t>(p.num_pages)) {
+                const int at = ahead & (p.page_size - 1);
+                const uint8_t* page = head + static_cast<uint64_t>(static_cast<uint32_t>(pg)) * page_stride;
+                const uint8_t* kc = page + (at * lay.kRow + 16 * lane);  // V's pair rows lie as far apart as two K rows
+                const uint8_t* vc = kc + lay.v_codes();
+#pragma unroll
+                for (int x = 0; x < D / 32; ++x) {
+                    cp_async16(ring_at + to + 512 * x, kc + 512 * x);
+                    cp_async16(v_at + to + 512 * x, vc + 512 * x);
+                }
+                if (lane < 4 * kBlocks) cp_async16(ring_at + to + S::kKs, page + (scale_at + at * kBlocks));
+            } else {
+                gone_bits |= 3u << (2 * stage);
+                if (lane == 0) report_index();
             }
         }
         cp_async_commit();
         ahead += 128;
     };
-    int pg0 = page_of(ahead), pg1 = page_of(ahead + 16);
+    int next_page = page_of(ahead);
 #pragma unroll
     for (unsigned i = 0; i < kStages - 1; ++i) {
-        const int n0 = page_of(ahead + 128), n1 = page_of(ahead + 144);
-        fetch(i, pg0, pg1);
-        pg0 = n0, pg1 = n1;
+        const int pg = next_page;
+        next_page = page_of(ahead + 128);
+        fetch(i, pg);
     }
 
     for (int r = warp; r < kRows; r += 4) {
@@ -337,37 +352,38 @@ __device__ __forceinline__ void few_unit(const AttendParams& p, FewShared<D, NT>
         __syncwarp();
         const unsigned gone2 = gone_bits >> (2 * stage);
         {
-            const int n0 = page_of(ahead + 128), n1 = page_of(ahead + 144);
-            fetch(stage == 0 ? kStages - 1 : stage - 1, pg0, pg1);
-            pg0 = n0, pg1 = n1;
+            const int pg = next_page;
+            next_page = page_of(ahead + 128);
+            fetch(stage == 0 ? kStages - 1 : stage - 1, pg);
         }
-        const uint8_t* st0 = ring + stage * 2 * S::kBytes;
+        const uint8_t* st0 = ring + stage * S::kBytes;
         stage = stage == kStages - 1 ? 0 : stage + 1;
 
-        // The scales are widened once for the warp, two (D = 64: one) K values and one pair of V values a lane
-        // and strip: block vb of tokens 2 vp, 2 vp + 1.  (e = 0, below the smallest normal, counts as 0.)
-        int ve[2][2];
+        // The scales are widened once for the warp, here two (D = 64: one) K values a lane and strip.  (e = 0,
+        // below the smallest normal, counts as 0.)
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-            const uint8_t* st = st0 + u * S::kBytes;
-            ve[u][0] = st[S::kVs + 2 * kBlocks * vp + vb], ve[u][1] = st[S::kVs + 2 * kBlocks * vp + kBlocks + vb];
+            const uint8_t* st = st0 + S::kKs + 16 * kBlocks * u;
             float* ks = &sm.kscale[warp][u][0][0];
             if constexpr (D == 128) {
-                const uint32_t w = *reinterpret_cast<const uint16_t*>(st + S::kKs + 2 * lane);
+                const uint32_t w = *reinterpret_cast<const uint16_t*>(st + 2 * lane);
                 *reinterpret_cast<float2*>(ks + 2 * lane) =
                     make_float2(__uint_as_float((w & 0xFFu) << 23), __uint_as_float((w << 15) & 0x7F800000u));
             } else {
-                ks[lane] = __uint_as_float(static_cast<uint32_t>(st[S::kKs + lane]) << 23);
+                ks[lane] = __uint_as_float(static_cast<uint32_t>(st[lane]) << 23);
             }
         }
         __syncwarp();
 
-#pragma unroll
+#pragma unroll 1
         for (int half = 0; half < 2; half += kSub) {
             float sc[kSub][NT][4];
+            int ve[kSub][2];  // scales of block vb of V's tokens 2 vp, 2 vp + 1
 #pragma unroll
             for (int u = 0; u < kSub; ++u) {
-                const uint8_t* st = st0 + (half + u) * S::kBytes;
+                const uint8_t* st = st0 + (half + u) * S::kStrip;
+                const uint8_t* vs = st0 + S::kVs + 16 * kBlocks * (half + u) + 2 * kBlocks * vp + vb;
+                ve[u][0] = vs[0], ve[u][1] = vs[kBlocks];
                 const float* ks = &sm.kscale[warp][half + u][0][0];
 #pragma unroll
                 for (int n = 0; n < NT; ++n) sc[u][n][0] = sc[u][n][1] = sc[u][n][2] = sc[u][n][3] = 0.0f;
@@ -429,11 +445,11 @@ __device__ __forceinline__ void few_unit(const AttendParams& p, FewShared<D, NT>
                     }
                     // what lies there may be anything: no scale of a token that no row sees is used
                     const int t = from + 16 * u + 2 * vp;
-                    if (gone || t < sp.first_lo || t > sp.last_hi) ve[half + u][0] = 0;
-                    if (gone || t + 1 < sp.first_lo || t + 1 > sp.last_hi) ve[half + u][1] = 0;
+                    if (gone || t < sp.first_lo || t > sp.last_hi) ve[u][0] = 0;
+                    if (gone || t + 1 < sp.first_lo || t + 1 > sp.last_hi) ve[u][1] = 0;
                 }
             }
-            int vmax = max(ve[half][0], ve[half][1]);
+            int vmax = max(ve[0][0], ve[0][1]);
             if constexpr (kSub == 2) vmax = max(vmax, max(ve[1][0], ve[1][1]));
 
             float top[NT][2];
@@ -483,12 +499,12 @@ __device__ __forceinline__ void few_unit(const AttendParams& p, FewShared<D, NT>
 #pragma unroll
             for (int u = 0; u < kSub; ++u)
                 sm.vscale[warp][half + u][vp][vb] =
-                    __viaddmin_s16x2_relu(static_cast<uint32_t>(ve[half + u][0] | ve[half + u][1] << 16), k2, 0x000F000Fu) << 10;
+                    __viaddmin_s16x2_relu(static_cast<uint32_t>(ve[u][0] | ve[u][1] << 16), k2, 0x000F000Fu) << 10;
             __syncwarp();
 
 #pragma unroll
             for (int u = 0; u < kSub; ++u) {
-                const uint8_t* st = st0 + (half + u) * S::kBytes;
+                const uint8_t* st = st0 + (half + u) * S::kStrip;
                 // softmax weights, transposed into fragments: tokens 2c, 2c + 1 (2c + 8, 2c + 9) of row g
                 uint32_t pt0[NT], pt1[NT];
 #pragma unroll
@@ -612,45 +628,48 @@ __global__ void __launch_bounds__(kFewThreads, few_resident(NT)) attend_few_kern
     constexpr int kRows = 8 * NT;
     griddep_launch_dependents();
     griddep_wait();
-    if (!p.ctas) {  // one unit
-        const int64_t block = blockIdx.x, bh = block / p.row_tiles;
-        const int b = static_cast<int>(bh / p.Hk);
-        const Sequence s = sequence_of(p, b);
-        const int r0 = static_cast<int>(block % p.row_tiles) * kRows;
-        const int nrows = min(kRows, s.nq * p.G - r0);
-        if (nrows <= 0) return;
-        const Span sp = span_of(p, s, r0, nrows);
-        const int begin = sp.first_lo >> kFewShift;
-        few_unit<D, NT>(p, sm, s, b, static_cast<int>(bh % p.Hk), r0, nrows, sp, begin, begin + blocks_of(sp, kFewShift), -1);
-        return;
+    Cut cut;
+    if (p.ctas) {
+        cut = cut_of(p, kFewShift, sm.scan, &sm.first_seq, &sm.first_pos);
+    } else {  // one unit
+        cut.b = static_cast<int>(blockIdx.x / p.row_tiles / p.Hk);
+        cut.pos = cut.seq_pos = 0, cut.end = 1;
     }
-    Cut cut = cut_of(p, kFewShift, sm.scan, &sm.first_seq, &sm.first_pos);
     while (cut.pos < cut.end) {
         const Sequence s = sequence_of(p, cut.b);
         const int rows = s.nq * p.G;
-        const int64_t per_head = sequence_blocks(p, s, kFewShift);
-        int64_t off = cut.pos - cut.seq_pos;
-        if (per_head == 0 || off >= per_head * p.Hk) {
-            cut.seq_pos += per_head * p.Hk;
-            ++cut.b;
-            continue;
-        }
-        const int kvh = static_cast<int>(off / per_head);
-        off -= kvh * per_head;
-        int r0 = 0, n = 0;
-        Span sp = {};
-        for (;; r0 += kRows) {
+        int kvh, r0, from, to;
+        int64_t slot = -1;
+        Span sp;
+        if (p.ctas) {
+            const int64_t per_head = sequence_blocks(p, s, kFewShift);
+            int64_t off = cut.pos - cut.seq_pos;
+            if (per_head == 0 || off >= per_head * p.Hk) {
+                cut.seq_pos += per_head * p.Hk;
+                ++cut.b;
+                continue;
+            }
+            kvh = static_cast<int>(off / per_head);
+            off -= kvh * per_head;
+            int n;
+            for (r0 = 0;; r0 += kRows) {
+                sp = span_of(p, s, r0, min(kRows, rows - r0));
+                n = blocks_of(sp, kFewShift);
+                if (off < n) break;
+                off -= n;
+            }
+            from = static_cast<int>(off), to = static_cast<int>(min(static_cast<int64_t>(n), off + cut.end - cut.pos));
+            cut.pos += to - from;
+            if (from != 0 || to != n) slot = 2 * static_cast<int64_t>(blockIdx.x) + (from == 0 ? 1 : 0);
+        } else {
+            kvh = static_cast<int>(blockIdx.x / p.row_tiles % p.Hk), r0 = static_cast<int>(blockIdx.x % p.row_tiles) * kRows;
+            if (r0 >= rows) return;
             sp = span_of(p, s, r0, min(kRows, rows - r0));
-            n = blocks_of(sp, kFewShift);
-            if (off < n) break;
-            off -= n;
+            from = 0, to = blocks_of(sp, kFewShift);
+            cut.pos = cut.end;
         }
-        const int from = static_cast<int>(off), to = static_cast<int>(min(static_cast<int64_t>(n), off + cut.end - cut.pos));
-        const bool whole = from == 0 && to == n;
-        const int64_t slot = whole ? -1 : 2 * static_cast<int64_t>(blockIdx.x) + (from == 0 ? 1 : 0);
         const int begin = sp.first_lo >> kFewShift;
         few_unit<D, NT>(p, sm, s, cut.b, kvh, r0, min(kRows, rows - r0), sp, begin + from, begin + to, slot);
-        cut.pos += to - from;
     }
 }
 
@@ -701,13 +720,21 @@ __global__ void __launch_bounds__(128) attend_join_kernel(const __grid_constant_
 #pragma unroll
     for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, x));
     float total = 0.0f, o[kElems] = {};
-    for (int k = 0; k < parts; ++k) {
-        const float2 ml = p.part_ml[place(k)];
-        const float w = ml.x == -INFINITY ? 0.0f : exp2_approx(ml.x - m) * ml.y;
-        const float* src = p.part_o + place(k) * D + kElems * lane;
-        total += w;
+    for (int k0 = 0; k0 < parts; k0 += 32) {
+        float w = 0.0f;  // of part k0 + lane
+        if (k0 + lane < parts) {
+            const float2 ml = p.part_ml[place(k0 + lane)];
+            if (ml.x != -INFINITY) w = exp2_approx(ml.x - m) * ml.y;
+        }
+        const int n = min(32, parts - k0);
+#pragma unroll 4
+        for (int k = 0; k < n; ++k) {
+            const float wk = __shfl_sync(0xFFFFFFFFu, w, k);
+            const float* src = p.part_o + place(k0 + k) * D + kElems * lane;
+            total += wk;
 #pragma unroll
-        for (int j = 0; j < kElems; ++j) o[j] += w == 0.0f ? 0.0f : w * src[j];
+            for (int j = 0; j < kElems; ++j) o[j] += wk == 0.0f ? 0.0f : wk * src[j];
+        }
     }
     const float inv = total > 0.0f ? kHadamardNorm / total : total == 0.0f ? 0.0f : total;
 #pragma unroll
