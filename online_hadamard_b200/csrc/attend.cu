@@ -14,6 +14,7 @@
 
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "common.cuh"
 #include "sm100.cuh"
@@ -42,7 +43,7 @@ struct AttendParams {
     float* lse;        // fp32 [T][Hq] or null
     // the split of the work (plan_attend): row tiles of tile_rows rows; `ctas` > 0: all blocks of keys of
     // all units in one row, cut into that many equal lengths (Cut); 0: one CTA per unit
-    int tile_rows, row_tiles, ctas;
+    int tile_rows, row_tiles, ctas, unit_cost;
     float* part_o;    // fp32 [ctas][2][tile_rows][D], each row divided by its own sum
     float2* part_ml;  // [ctas][2][tile_rows]: its reference m (base 2) and sum of 2^(s - m)
 };
@@ -81,75 +82,131 @@ __device__ __forceinline__ Span span_of(const AttendParams& p, const Sequence& s
     return {first_key(p, a), first_key(p, z), a, z};
 }
 
-// A unit is a (sequence, kv head, tile of query rows); its work is its span in blocks of 2^shift keys.
+// A unit is a (sequence, tile of query rows, kv head); its work is its span in blocks of 2^shift keys (one
+// block where nothing is seen).
 __device__ __forceinline__ int blocks_of(const Span& sp, int shift) {
-    return sp.last_hi < 0 ? 0 : (sp.last_hi >> shift) - (sp.first_lo >> shift) + 1;
+    return sp.last_hi < 0 ? 1 : (sp.last_hi >> shift) - (sp.first_lo >> shift) + 1;
 }
-// Blocks of all row tiles of one kv head of a sequence.
-__device__ __forceinline__ int64_t sequence_blocks(const AttendParams& p, const Sequence& s, int shift) {
-    int64_t n = 0;
-    const int rows = s.nq * p.G;
-    for (int r0 = 0; r0 < rows; r0 += p.tile_rows) n += blocks_of(span_of(p, s, r0, min(p.tile_rows, rows - r0)), shift);
-    return n;
+struct Tile {  // of a sequence; nrows <= 0: none
+    Sequence s;
+    Span sp;
+    int b, r0, nrows, blocks;
+};
+__device__ __forceinline__ Tile tile_of(const AttendParams& p, int64_t item, int shift) {
+    Tile t;
+    t.b = static_cast<int>(p.row_tiles == 1 ? item : item / p.row_tiles);
+    t.r0 = static_cast<int>(item - static_cast<int64_t>(t.b) * p.row_tiles) * p.tile_rows;
+    t.s = sequence_of(p, t.b);
+    t.nrows = min(p.tile_rows, t.s.nq * p.G - t.r0);
+    t.sp = span_of(p, t.s, t.r0, max(t.nrows, 1));
+    t.blocks = t.nrows > 0 ? blocks_of(t.sp, shift) : 0;
+    return t;
 }
 
 // Sequences are of unequal length, known on the device only, and few units leave most of the GPU idle: so
-// the blocks of all units stand in one row (sequence, then kv head, then row tile), and CTA i of the
-// resident ones takes [i len, (i + 1) len) of it, whatever units those belong to.  A unit that one CTA holds
-// whole is written directly, parts of one are joined by attend_join_kernel.  A CTA cuts at most two units:
-// its parts go to slot 0 (the unit that its range begins in) and slot 1 (the one it ends in).  No CTA gets
-// less than kMinKeys keys (joining would cost more than it saves).
+// the blocks of all units stand in one row (tiles, then their kv heads), each unit behind `unit_cost` empty
+// places for what starting and ending it costs, and CTA i of the resident ones takes the places [i len,
+// (i + 1) len), whatever units they belong to.  A unit that one CTA holds whole is written directly, parts of one
+// are joined by attend_join_kernel.  A CTA cuts at most two units: its parts go to slot 0 (the unit that its
+// range begins in) and slot 1 (the one it ends in).  No range is shorter than kMinKeys keys (joining would
+// cost more than it saves).
 constexpr int kMinKeys = 128;
-__device__ __forceinline__ int64_t cut_length(const AttendParams& p, int64_t total, int shift) {
-    const int64_t len = (total + p.ctas - 1) / p.ctas;
-    return len > (kMinKeys >> shift) ? len : (kMinKeys >> shift);
+__device__ __forceinline__ int64_t tile_places(const AttendParams& p, const Tile& t) {
+    return t.nrows > 0 ? static_cast<int64_t>(t.blocks + p.unit_cost) * p.Hk : 0;
 }
-
-struct Cut {
-    int64_t pos, end;  // this CTA's range
-    int b;             // the sequence that pos lies in, and where that sequence begins
-    int64_t seq_pos;
+struct Place {  // the tile that a place lies in, and where that tile begins
+    int64_t pos, len, total;
+    int64_t item, item_pos;
 };
-// By all 128 threads of a CTA: thread i adds up its share of the sequences, the one whose share holds the
-// CTA's first block walks it.
-__device__ __forceinline__ Cut cut_of(const AttendParams& p, int shift, int64_t* scan, int* first_seq, int64_t* first_pos) {
+struct PlaceShared {
+    int64_t scan[32], item, item_pos;
+};
+// Place i len, by all THREADS threads of a CTA: a thread adds up its share of the tiles, the one whose share
+// holds the place walks it.
+template <int THREADS>
+__device__ __forceinline__ Place find_place(const AttendParams& p, int shift, int64_t i, PlaceShared& sm) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int share = (p.B + 127) / 128, b0 = min(p.B, static_cast<int>(threadIdx.x) * share), b1 = min(p.B, b0 + share);
+    const int64_t items = static_cast<int64_t>(p.B) * p.row_tiles, share = (items + THREADS - 1) / THREADS;
+    const int64_t a = min(items, threadIdx.x * share), z = min(items, a + share);
     int64_t mine = 0;
-    for (int b = b0; b < b1; ++b) mine += sequence_blocks(p, sequence_of(p, b), shift) * p.Hk;
+    for (int64_t x = a; x < z; ++x) mine += tile_places(p, tile_of(p, x, shift));
     int64_t upto = mine;
 #pragma unroll
     for (int x = 1; x < 32; x <<= 1) {
         const int64_t y = __shfl_up_sync(0xFFFFFFFFu, upto, x);
         if (lane >= x) upto += y;
     }
-    if (lane == 31) scan[warp] = upto;
+    if (lane == 31) sm.scan[warp] = upto;
     __syncthreads();
-    int64_t total = 0;
-#pragma unroll
-    for (int w = 0; w < 4; ++w) {
-        if (w < warp) upto += scan[w];
-        total += scan[w];
+    Place c;
+    c.total = 0;
+#pragma unroll 4
+    for (int w = 0; w < THREADS / 32; ++w) {
+        if (w < warp) upto += sm.scan[w];
+        c.total += sm.scan[w];
     }
-    const int64_t len = cut_length(p, total, shift);
-    Cut c;
-    c.pos = static_cast<int64_t>(blockIdx.x) * len;
-    c.end = c.pos + len < total ? c.pos + len : total;
+    const int64_t len = (c.total + p.ctas - 1) / p.ctas;
+    c.len = len > (kMinKeys >> shift) ? len : (kMinKeys >> shift);
+    c.pos = i * c.len;
     if (c.pos < upto && c.pos >= upto - mine) {
         int64_t at = upto - mine;
-        for (int b = b0; b < b1; ++b) {
-            const int64_t n = sequence_blocks(p, sequence_of(p, b), shift) * p.Hk;
+        for (int64_t x = a; x < z; ++x) {
+            const int64_t n = tile_places(p, tile_of(p, x, shift));
             if (c.pos < at + n) {
-                *first_seq = b, *first_pos = at;
+                sm.item = x, sm.item_pos = at;
                 break;
             }
             at += n;
         }
     }
     __syncthreads();
-    c.b = *first_seq, c.seq_pos = *first_pos;
+    c.item = sm.item, c.item_pos = sm.item_pos;
     return c;
 }
+
+// The units of a CTA in order, as parts [begin, end) in block numbers; slot < 0: whole.
+struct Unit {
+    Tile t;
+    int kvh, begin, end;
+    int64_t slot;
+};
+struct Walk {
+    int64_t pos, end, item, item_pos;
+    Walk() = default;
+    __device__ __forceinline__ Walk(const AttendParams& p, const Place& c)
+        : pos(c.pos), end(c.pos + c.len < c.total ? c.pos + c.len : c.total), item(c.item), item_pos(c.item_pos) {}
+    __device__ __forceinline__ Walk(int64_t unit, int Hk) : pos(unit % Hk), end(-1), item(unit / Hk), item_pos(0) {}
+    __device__ __forceinline__ bool next(const AttendParams& p, int shift, Unit& u) {
+        if (!p.ctas) {  // one unit
+            if (end == 0) return false;
+            end = 0;
+            u.t = tile_of(p, item, shift);
+            u.kvh = static_cast<int>(pos);
+            u.begin = u.t.sp.first_lo >> shift, u.end = u.begin + u.t.blocks, u.slot = -1;
+            return u.t.nrows > 0;
+        }
+        while (pos < end) {
+            u.t = tile_of(p, item, shift);
+            const int64_t places = tile_places(p, u.t), off = pos - item_pos;
+            if (off >= places) {
+                item_pos += places;
+                ++item;
+                continue;
+            }
+            const int per = u.t.blocks + p.unit_cost;
+            u.kvh = static_cast<int>(off / per);
+            const int x0 = static_cast<int>(off - static_cast<int64_t>(u.kvh) * per);
+            const int x1 = static_cast<int>(min(static_cast<int64_t>(per), x0 + end - pos));
+            pos += x1 - x0;
+            const int from = max(0, x0 - p.unit_cost), to = max(0, x1 - p.unit_cost);
+            if (to <= from) continue;
+            u.begin = (u.t.sp.first_lo >> shift) + from, u.end = u.begin + to - from;
+            u.slot = from == 0 && to == u.t.blocks ? -1 : 2 * static_cast<int64_t>(blockIdx.x) + (from == 0 ? 1 : 0);
+            return true;
+        }
+        return false;
+    }
+};
 
 // Query rows are brought to f16 by a power of two of their own: |q| < 2^(E - 126) for the row's largest
 // exponent E, so |FWHT32(q) c0| 2^(138 - E) < sqrt(32) 2^12 fits, and elements keep their 11 bits down to
@@ -211,29 +268,39 @@ struct FewShared {
     static constexpr int kBlocks = D / 32;
     static constexpr size_t kRing = 4 * kStages * TokenBlock<D>::kBytes, kJoin = 4 * 8 * D * sizeof(float);
     alignas(16) uint8_t ring[kRing > kJoin ? kRing : kJoin];  // in the end the warps' sums of 8 rows
-    alignas(16) __half q[8 * NT][D + 8];
-    alignas(16) float kscale[4][2][16][kBlocks];    // a warp's strips: 2^(e - 127) of K's blocks
-    alignas(16) uint32_t vscale[4][2][8][kBlocks];  // f16 2^(e - vref) of V's, two tokens
+    struct Scales {
+        alignas(16) float k[4][2][16][kBlocks];    // a warp's strips: 2^(e - 127) of K's blocks
+        alignas(16) uint32_t v[4][2][8][kBlocks];  // f16 2^(e - vref) of V's, two tokens
+    };
+    struct Both {
+        Scales scale;
+        alignas(16) __half q[8 * NT][D + 8];
+    };
+    union Either {  // 8 rows of Q go to registers before the first block
+        Scales scale;
+        alignas(16) __half q[8 * NT][D + 8];
+    };
+    typename std::conditional<NT == 1, Either, Both>::type u;
     float factor[8 * NT];
     int lo[8 * NT], hi[8 * NT];
     float2 ml[4][8];
     float vref[4];
-    int64_t scan[4];
-    int first_seq;
-    int64_t first_pos;
+    PlaceShared place;
 };
 
-// One unit, blocks [begin, end) of its span (absolute block numbers); slot < 0: the result itself.
 template <int D, int NT>
-__device__ __forceinline__ void few_unit(const AttendParams& p, FewShared<D, NT>& sm, const Sequence& s, int b, int kvh,
-                                         int r0, int nrows, const Span& sp, int begin, int end, int64_t slot) {
+__device__ __forceinline__ void few_unit(const AttendParams& p, FewShared<D, NT>& sm, const Unit& unit) {
+    const Sequence& s = unit.t.s;
+    const Span& sp = unit.t.sp;
+    const int kvh = unit.kvh, r0 = unit.t.r0, nrows = unit.t.nrows, begin = unit.begin, end = unit.end;
+    const int64_t slot = unit.slot;
     using S = TokenBlock<D>;
     constexpr int kBlocks = D / 32, kRows = 8 * NT;
     constexpr int kSub = NT == 4 ? 1 : 2;  // strips worked on together, as registers allow
     const int lane = threadIdx.x & 31, warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0);
     const int g = lane >> 2, c = lane & 3;
     const int count = max(0, (end - begin - warp + 3) >> 2);  // blocks of this warp
-    const int32_t* table = p.tables + b * p.table_width;
+    const int32_t* table = p.tables + unit.t.b * p.table_width;
     uint8_t* ring = sm.ring + warp * kStages * S::kBytes;
     unsigned gone_bits = 0;  // bits 2 stage + u: strips (16 tokens) that were not copied
     // what a lane copies: 16 bytes of every 512 of the codes, and a piece of the scales
@@ -246,7 +313,7 @@ __device__ __forceinline__ void few_unit(const AttendParams& p, FewShared<D, NT>
     const int scale_at = lane < 2 * kBlocks ? lay.k_scales() + 16 * lane : lay.v_scales() + 16 * (lane - 2 * kBlocks);
     int ahead = (begin + warp) * 32;  // first token of the block to fetch next
     const int fetch_end = end * 32;
-    auto page_of = [&](int t) { return t < fetch_end ? table[t >> p.page_shift] : -1; };
+    auto page_of = [&](int t) { return t < fetch_end && t <= sp.last_hi ? table[t >> p.page_shift] : -1; };
     auto fetch = [&](unsigned stage, int pg) {
         if (ahead < fetch_end) {
             const uint32_t to = stage * S::kBytes;
@@ -286,7 +353,7 @@ __device__ __forceinline__ void few_unit(const AttendParams& p, FewShared<D, NT>
                 if (lane < 4 * kBlocks) cp_async16(ring_at + to + S::kKs, page + (scale_at + at * kBlocks));
             } else {
                 gone_bits |= 3u << (2 * stage);
-                if (lane == 0) report_index();
+                if (ahead <= sp.last_hi && lane == 0) report_index();
             }
         }
         cp_async_commit();
@@ -316,7 +383,7 @@ __device__ __forceinline__ void few_unit(const AttendParams& p, FewShared<D, NT>
         const float mul = query_multiplier(E);
 #pragma unroll
         for (int i = 0; i < kBlocks; ++i)
-            sm.q[r][32 * i + lane] = __float2half_rn(warp_fwht32(x[i] * mul, lane) * kHadamardNorm);
+            sm.u.q[r][32 * i + lane] = __float2half_rn(warp_fwht32(x[i] * mul, lane) * kHadamardNorm);
         if (lane == 0) {
             sm.factor[r] = score_factor(p.scale_log2, E);
             sm.lo[r] = first_key(p, s.pos0 + qi);
@@ -329,7 +396,8 @@ __device__ __forceinline__ void few_unit(const AttendParams& p, FewShared<D, NT>
     uint4 qf[kBlocks];
     if constexpr (NT == 1) {
 #pragma unroll
-        for (int i = 0; i < kBlocks; ++i) qf[i] = *reinterpret_cast<const uint4*>(&sm.q[g][32 * i + 8 * c]);
+        for (int i = 0; i < kBlocks; ++i) qf[i] = *reinterpret_cast<const uint4*>(&sm.u.q[g][32 * i + 8 * c]);
+        __syncthreads();
     }
     float f[NT][2], ref[NT][2], bound[NT][2], sum[NT][2], o[NT][2 * kBlocks][4];
     const int vp = D == 128 ? lane >> 2 : (lane >> 1) & 7, vb = lane & (kBlocks - 1);
@@ -364,7 +432,7 @@ __device__ __forceinline__ void few_unit(const AttendParams& p, FewShared<D, NT>
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
             const uint8_t* st = st0 + S::kKs + 16 * kBlocks * u;
-            float* ks = &sm.kscale[warp][u][0][0];
+            float* ks = &sm.u.scale.k[warp][u][0][0];
             if constexpr (D == 128) {
                 const uint32_t w = *reinterpret_cast<const uint16_t*>(st + 2 * lane);
                 *reinterpret_cast<float2*>(ks + 2 * lane) =
@@ -384,7 +452,7 @@ __device__ __forceinline__ void few_unit(const AttendParams& p, FewShared<D, NT>
                 const uint8_t* st = st0 + (half + u) * S::kStrip;
                 const uint8_t* vs = st0 + S::kVs + 16 * kBlocks * (half + u) + 2 * kBlocks * vp + vb;
                 ve[u][0] = vs[0], ve[u][1] = vs[kBlocks];
-                const float* ks = &sm.kscale[warp][half + u][0][0];
+                const float* ks = &sm.u.scale.k[warp][half + u][0][0];
 #pragma unroll
                 for (int n = 0; n < NT; ++n) sc[u][n][0] = sc[u][n][1] = sc[u][n][2] = sc[u][n][3] = 0.0f;
                 uint32_t k0[kBlocks], k1[kBlocks];
@@ -417,7 +485,7 @@ __device__ __forceinline__ void few_unit(const AttendParams& p, FewShared<D, NT>
                         if constexpr (NT == 1)
                             q = qf[j];
                         else
-                            q = *reinterpret_cast<const uint4*>(&sm.q[8 * n + g][32 * j + 8 * c]);
+                            q = *reinterpret_cast<const uint4*>(&sm.u.q[8 * n + g][32 * j + 8 * c]);
                         float acc[4];
                         mma_f16_16x8x16_first(acc, a[0], z[0], a[1], z[1], q.x, q.y);
                         mma_f16_16x8x16(acc, a[2], z[2], a[3], z[3], q.z, q.w);
@@ -498,7 +566,7 @@ __device__ __forceinline__ void few_unit(const AttendParams& p, FewShared<D, NT>
             const uint32_t k2 = static_cast<uint32_t>((15 - vref) & 0xFFFF) * 0x00010001u;
 #pragma unroll
             for (int u = 0; u < kSub; ++u)
-                sm.vscale[warp][half + u][vp][vb] =
+                sm.u.scale.v[warp][half + u][vp][vb] =
                     __viaddmin_s16x2_relu(static_cast<uint32_t>(ve[u][0] | ve[u][1] << 16), k2, 0x000F000Fu) << 10;
             __syncwarp();
 
@@ -520,7 +588,7 @@ __device__ __forceinline__ void few_unit(const AttendParams& p, FewShared<D, NT>
                 }
                 uint32_t va[4], vz[4];  // pairs c and c + 4: (first token: blocks 01, 23), (second token: 01, 23)
                 uint32_t vx0[kBlocks], vx1[kBlocks];
-                const uint32_t* vs = &sm.vscale[warp][half + u][0][0];
+                const uint32_t* vs = &sm.u.scale.v[warp][half + u][0][0];
                 if constexpr (D == 128) {
                     const uint4 a = *reinterpret_cast<const uint4*>(st + S::kV + 16 * S::v_piece(c, g));
                     const uint4 z = *reinterpret_cast<const uint4*>(st + S::kV + 16 * S::v_piece(c + 4, g));
@@ -625,141 +693,699 @@ template <int D, int NT>
 __global__ void __launch_bounds__(kFewThreads, few_resident(NT)) attend_few_kernel(const __grid_constant__ AttendParams p) {
     extern __shared__ uint4 dynamic_smem[];
     FewShared<D, NT>& sm = *reinterpret_cast<FewShared<D, NT>*>(dynamic_smem);
-    constexpr int kRows = 8 * NT;
     griddep_launch_dependents();
     griddep_wait();
-    Cut cut;
-    if (p.ctas) {
-        cut = cut_of(p, kFewShift, sm.scan, &sm.first_seq, &sm.first_pos);
-    } else {  // one unit
-        cut.b = static_cast<int>(blockIdx.x / p.row_tiles / p.Hk);
-        cut.pos = cut.seq_pos = 0, cut.end = 1;
+    const Place place = p.ctas ? find_place<kFewThreads>(p, kFewShift, blockIdx.x, sm.place) : Place{};
+    Walk walk = p.ctas ? Walk(p, place) : Walk(blockIdx.x, p.Hk);
+    Unit unit;
+    while (walk.next(p, kFewShift, unit)) few_unit<D, NT>(p, sm, unit);
+}
+
+// ------------------------------------------------------------------------------ many query rows
+//
+// Persistent CTAs of five warpgroups, one per SM, on units of 256 rows (two tensor-core tiles of 128) and
+// blocks of 128 keys:
+//   warpgroups 0, 1  softmax of one tile each, a thread a row: scores out of tensor memory, weights (f16) back
+//                    in their place, the tile's sums rescaled there when the reference moves; before that
+//                    the rows' queries (transform, f16, shared memory), after it the results
+//   warpgroup 2      K: codes to f16 in shared memory, K-major
+//   warpgroup 3      V: likewise, elements along the rows (MN-major, as V's codes lie)
+//   warp 16          issues S_t = Q_t K^T and O_t += P_t V (tcgen05, f16 operands, fp32 sums)
+// so the two tiles' matrix products and exponentials alternate, and the codes of the next blocks are widened
+// meanwhile.  In tensor memory stand S_0, S_1 (each 128 columns, its first 64 then P) and O_0, O_1.
+// E2M1 times a power of two is exact in f16: K is held relative to the largest scale of a warp's 32 tokens (which
+// goes into those columns' score factor), V relative to a reference above the largest scale met (rescaled like
+// the softmax reference when it moves), with 2^12 on top, so scales down to 2^-26 of the largest are exact.
+constexpr int kManyShift = 7;
+constexpr int kManyRows = 256;
+constexpr int kManyThreads = 640;
+// Registers of a thread: 96 at launch (640 threads), then split 160 / 64 / 32 (softmax / codes / products).
+constexpr int kManyLaunchRegs = 96, kSoftmaxRegs = 160, kCodeRegs = 64, kIssueRegs = 32;
+static_assert(2 * kSoftmaxRegs + 2 * kCodeRegs + kIssueRegs <= 5 * kManyLaunchRegs, "registers of a CTA");
+constexpr int kOperandLift = 12;
+
+template <int D>
+struct ManyShared {
+    static constexpr int kTile = 128 * D * 2;  // bytes of 128 rows of f16, in panels of 64 elements (16 KB)
+    static constexpr int kRaw = 16 * D + 32 * (D / 32);  // codes and scales of a warp's 32 tokens of K or V
+    alignas(1024) uint8_t q[2][kTile];
+    alignas(1024) uint8_t k[2][kTile];
+    alignas(1024) uint8_t v[2][kTile];
+    alignas(16) uint8_t raw[8][kRaw];
+    uint64_t k_full[2], k_free[2], v_full[2], v_free[2], q_full[2], s_full[2], p_full[2], o_full[2], r_full[4], drained;
+    // of block j at [j % 4]: each K warp's largest scale and its strips (16 tokens) whose page is not there,
+    // and V's reference; a slot is rewritten after the products of block j + 2, whose softmax follows that of j.  r_full: V's is there
+    int k_ref[4][4], gone[4][4], v_ref[4];
+    int v_top[4];
+    int abort;
+    uint32_t tmem;
+    PlaceShared place;
+    // each warp's walk through the CTA's units, kept here to spare registers
+    struct Course {
+        Walk walk;
+        Unit unit;
+    } course[17];
+};
+
+// The warp's next unit.
+template <int D>
+__device__ __forceinline__ bool next_unit(const AttendParams& p, typename ManyShared<D>::Course& c, int lane) {
+    bool more = false;
+    __syncwarp();
+    if (lane == 0) more = c.walk.next(p, kManyShift, c.unit);
+    return __shfl_sync(0xFFFFFFFFu, more, 0);
+}
+
+// mbar_wait with one answer for the whole warp.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int* abort) {
+    const bool ok = mbar_wait(bar, parity, abort);
+    return __all_sync(0xFFFFFFFFu, ok);
+}
+
+__device__ __forceinline__ void group_sync(int id) { asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory"); }
+
+// Codes of a warp's 32 tokens of K or V on their way through shared memory, one block ahead; the pages' numbers
+// two blocks ahead.
+template <int D, bool IS_V>
+struct CodeStream {
+    static constexpr int kBlocks = D / 32;
+    const AttendParams& p;
+    typename ManyShared<D>::Course& course;
+    const Unit& unit;
+    bool more;
+    int block;        // of the request after the pending one
+    int32_t page[2];  // its pages (of its first and second 16 tokens)
+    uint32_t there;   // strips of the pending request that were copied, that are seen
+    uint32_t seen;
+    int first, last;  // the tokens of the pending request that any row sees, relative to its first
+    int w, lane;
+
+    __device__ __forceinline__ CodeStream(const AttendParams& p_, typename ManyShared<D>::Course& c, int w_, int lane_)
+        : p(p_), course(c), unit(c.unit), w(w_), lane(lane_) {
+        more = next_unit<D>(p, course, lane);
+        if (more) block = unit.begin;
+        look();
     }
-    while (cut.pos < cut.end) {
-        const Sequence s = sequence_of(p, cut.b);
-        const int rows = s.nq * p.G;
-        int kvh, r0, from, to;
-        int64_t slot = -1;
-        Span sp;
-        if (p.ctas) {
-            const int64_t per_head = sequence_blocks(p, s, kFewShift);
-            int64_t off = cut.pos - cut.seq_pos;
-            if (per_head == 0 || off >= per_head * p.Hk) {
-                cut.seq_pos += per_head * p.Hk;
-                ++cut.b;
-                continue;
+    __device__ __forceinline__ void look() {
+        page[0] = page[1] = -1;
+        if (!more) return;
+        const int t = block * 128 + 32 * w;
+        const int32_t* table = p.tables + unit.t.b * p.table_width;
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+            if (t + 16 * u <= unit.t.sp.last_hi && t + 16 * u + 15 >= unit.t.sp.first_lo)
+                page[u] = table[(t + 16 * u) >> p.page_shift];
+    }
+    // Starts the copies of the next block and looks further.
+    __device__ __forceinline__ void request(uint8_t* raw) {
+        if (more) {
+            const int t0 = block * 128 + 32 * w;
+            const PageLayout<D> lay{p.page_size};
+            there = seen = 0;
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const int t = t0 + 16 * u;
+                if (t > unit.t.sp.last_hi || t + 15 < unit.t.sp.first_lo) continue;
+                seen |= 1u << u;
+                if (static_cast<unsigned>(page[u]) >= static_cast<uint64_t>(p.num_pages)) {
+                    if (lane == 0) report_index();
+                    continue;
+                }
+                there |= 1u << u;
+                const int at = t & (p.page_size - 1);
+                const uint8_t* src = p.cache + (static_cast<int64_t>(page[u]) * p.Hk + unit.kvh) * lay.bytes();
+                const uint8_t* codes = src + (IS_V ? lay.v_codes() : 0) + at * lay.kRow + 16 * lane;
+#pragma unroll
+                for (int x = 0; x < D / 64; ++x) {
+                    const int piece = lane + 32 * x;  // V's pieces swizzled as its readers want them
+                    const int to = !IS_V ? piece
+                                   : D == 128 ? (piece / 8) * 8 + ((piece % 8) ^ ((piece / 8 & 3) * 2))
+                                              : (piece / 4) * 4 + ((piece % 4) ^ ((piece / 8 & 1) * 2));
+                    cp_async16(smem_u32(raw) + u * 8 * D + 16 * to, codes + 512 * x);
+                }
+                if (lane < kBlocks)
+                    cp_async16(smem_u32(raw) + 16 * D + 16 * kBlocks * u + 16 * lane,
+                               src + (IS_V ? lay.v_scales() : lay.k_scales()) + at * kBlocks + 16 * lane);
             }
-            kvh = static_cast<int>(off / per_head);
-            off -= kvh * per_head;
-            int n;
-            for (r0 = 0;; r0 += kRows) {
-                sp = span_of(p, s, r0, min(kRows, rows - r0));
-                n = blocks_of(sp, kFewShift);
-                if (off < n) break;
-                off -= n;
+            first = unit.t.sp.first_lo - t0, last = unit.t.sp.last_hi - t0;
+            if (++block == unit.end) {
+                more = next_unit<D>(p, course, lane);
+                if (more) block = unit.begin;
             }
-            from = static_cast<int>(off), to = static_cast<int>(min(static_cast<int64_t>(n), off + cut.end - cut.pos));
-            cut.pos += to - from;
-            if (from != 0 || to != n) slot = 2 * static_cast<int64_t>(blockIdx.x) + (from == 0 ? 1 : 0);
-        } else {
-            kvh = static_cast<int>(blockIdx.x / p.row_tiles % p.Hk), r0 = static_cast<int>(blockIdx.x % p.row_tiles) * kRows;
-            if (r0 >= rows) return;
-            sp = span_of(p, s, r0, min(kRows, rows - r0));
-            from = 0, to = blocks_of(sp, kFewShift);
-            cut.pos = cut.end;
+            look();
         }
-        const int begin = sp.first_lo >> kFewShift;
-        few_unit<D, NT>(p, sm, s, cut.b, kvh, r0, min(kRows, rows - r0), sp, begin + from, begin + to, slot);
+        cp_async_commit();
+    }
+};
+
+// 16 bytes of f16: eight codes times a power of two.
+__device__ __forceinline__ uint4 widen_codes(uint32_t codes, uint32_t scale2) {
+    uint32_t h[4];
+    e2m1x8_to_f16(codes, h);
+    const __half2 s = *reinterpret_cast<const __half2*>(&scale2);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __half2 x = __hmul2(*reinterpret_cast<const __half2*>(&h[i]), s);
+        h[i] = *reinterpret_cast<const uint32_t*>(&x);
+    }
+    return make_uint4(h[0], h[1], h[2], h[3]);
+}
+// f16 2^(e - ref + kOperandLift) in both halves, 0 below the smallest normal (e <= ref).
+__device__ __forceinline__ uint32_t operand_scale(uint32_t e, int ref) {
+    return static_cast<uint32_t>(max(static_cast<int>(e) - ref + 15 + kOperandLift, 0)) * 0x04000400u;
+}
+__device__ __forceinline__ int byte_max(uint32_t w) {
+    return max(max(w & 0xFFu, (w >> 8) & 0xFFu), max((w >> 16) & 0xFFu, w >> 24));
+}
+
+template <int D>
+__device__ __forceinline__ void many_keys(const AttendParams& p, ManyShared<D>& sm, int w, int lane) {
+    constexpr int kBlocks = D / 32;
+    uint8_t* raw = sm.raw[w];
+    CodeStream<D, false> cs(p, sm.course[8 + w], w, lane);
+    bool pending = cs.more;
+    cs.request(raw);
+    // lane (token, chunk c of 8 elements a block): 8 tokens a step; the tokens of 8 neighbouring lanes differ by 4,
+    // so that their 16-byte stores meet 8 different banks of the swizzled rows
+    const int c = lane & 3, tok = ((lane >> 2) & 1) * 4 + (lane >> 3);
+    for (int j = 0; pending; ++j) {
+        uint32_t code[4][kBlocks], scale[4];
+        cp_async_wait<0>();
+        __syncwarp();
+        int top = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int t = 8 * i + tok;
+            const bool use = t >= cs.first && t <= cs.last && ((cs.there >> (i >> 1)) & 1u);
+            if constexpr (D == 128) {
+                const uint4 x = *reinterpret_cast<const uint4*>(raw + t * 64 + 16 * c);
+                code[i][0] = x.x, code[i][1] = x.y, code[i][2] = x.z, code[i][3] = x.w;
+                scale[i] = *reinterpret_cast<const uint32_t*>(raw + 16 * D + 4 * t);
+            } else {
+                const uint2 x = *reinterpret_cast<const uint2*>(raw + t * 32 + 8 * c);
+                code[i][0] = x.x, code[i][1] = x.y;
+                scale[i] = *reinterpret_cast<const uint16_t*>(raw + 16 * D + 2 * t);
+            }
+            if (!use) {  // whatever lay there: zeros
+                scale[i] = 0;
+#pragma unroll
+                for (int b = 0; b < kBlocks; ++b) code[i][b] = 0;
+            }
+            top = max(top, byte_max(scale[i]));
+        }
+        const uint32_t gone = cs.seen & ~cs.there;
+        __syncwarp();
+        pending = cs.more;
+        cs.request(raw);
+        const int ref = static_cast<int>(__reduce_max_sync(0xFFFFFFFFu, static_cast<unsigned>(top)));
+        const int stage = j & 1;
+        if (j >= 2 && !warp_wait(&sm.k_free[stage], ((j >> 1) & 1) ^ 1, &sm.abort)) break;
+        if (lane == 0) sm.k_ref[j & 3][w] = ref, sm.gone[j & 3][w] = static_cast<int>(gone);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int row = 32 * w + 8 * i + tok;
+#pragma unroll
+            for (int b = 0; b < kBlocks; ++b) {
+                const uint32_t s2 = operand_scale((scale[i] >> (8 * b)) & 0xFFu, ref);
+                const int chunk = (4 * (b & 1) + c) ^ (row & 7);
+                *reinterpret_cast<uint4*>(sm.k[stage] + (b >> 1) * 16384 + row * 128 + chunk * 16) = widen_codes(code[i][b], s2);
+            }
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(&sm.k_full[stage]);
+    }
+    cp_async_wait<0>();
+}
+
+template <int D>
+__device__ __forceinline__ void many_values(const AttendParams& p, ManyShared<D>& sm, int w, int lane) {
+    constexpr int kBlocks = D / 32, kWords = kBlocks / 2;
+    uint8_t* raw = sm.raw[4 + w];
+    CodeStream<D, true> cs(p, sm.course[12 + w], w, lane);
+    bool pending = cs.more;
+    cs.request(raw);
+    // lane (pair of tokens, elements 8c .. 8c + 7 of each block): 8 pairs a step; 8 neighbouring lanes are 4 pairs
+    // by 2 chunks, whose 16-byte stores meet 8 different banks
+    const int c = ((lane >> 2) & 1) + ((lane >> 3) & 1) * 2, pr = (lane & 3) + (lane >> 4) * 4;
+    int ref = 0;
+    for (int j = 0; pending; ++j) {
+        uint32_t code[2][4 * kWords], scale[2][2];
+        cp_async_wait<0>();
+        __syncwarp();
+        int top = 0;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int pair = 8 * i + pr;
+            if constexpr (D == 128) {
+                const int s = (pair & 3) * 2;
+                const uint4 x = *reinterpret_cast<const uint4*>(raw + pair * 128 + 16 * ((2 * c) ^ s));
+                const uint4 y = *reinterpret_cast<const uint4*>(raw + pair * 128 + 16 * ((2 * c + 1) ^ s));
+                code[i][0] = x.x, code[i][1] = x.y, code[i][2] = x.z, code[i][3] = x.w;
+                code[i][4] = y.x, code[i][5] = y.y, code[i][6] = y.z, code[i][7] = y.w;
+                const uint2 e = *reinterpret_cast<const uint2*>(raw + 16 * D + 8 * pair);
+                scale[i][0] = e.x, scale[i][1] = e.y;
+            } else {
+                const uint4 x = *reinterpret_cast<const uint4*>(raw + pair * 64 + 16 * (c ^ ((pair >> 1 & 1) * 2)));
+                code[i][0] = x.x, code[i][1] = x.y, code[i][2] = x.z, code[i][3] = x.w;
+                const uint32_t e = *reinterpret_cast<const uint32_t*>(raw + 16 * D + 4 * pair);
+                scale[i][0] = e & 0xFFFFu, scale[i][1] = e >> 16;
+            }
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const int t = 2 * pair + r;
+                if (t < cs.first || t > cs.last || !((cs.there >> i) & 1u)) {  // whatever lay there: zeros
+                    scale[i][r] = 0;
+#pragma unroll
+                    for (int x = 0; x < kWords; ++x) code[i][r * kWords + x] = code[i][(2 + r) * kWords + x] = 0;
+                }
+                top = max(top, byte_max(scale[i][r]));
+            }
+        }
+        __syncwarp();
+        pending = cs.more;
+        cs.request(raw);
+        top = static_cast<int>(__reduce_max_sync(0xFFFFFFFFu, static_cast<unsigned>(top)));
+        const int stage = j & 1;
+        // all four warps go on or none does (kNoBlock in one of them: its wait gave up)
+        constexpr int kNoBlock = 1 << 20;
+        if (j >= 2 && !warp_wait(&sm.v_free[stage], ((j >> 1) & 1) ^ 1, &sm.abort)) top = kNoBlock;
+        if (lane == 0) sm.v_top[w] = top;
+        group_sync(2);
+        top = max(max(sm.v_top[0], sm.v_top[1]), max(sm.v_top[2], sm.v_top[3]));
+        group_sync(2);
+        if (top == kNoBlock) break;
+        if (top > ref) ref = min(top + 3, 254);  // room for three doublings before the next time
+        if (lane == 0 && w == 0) {
+            sm.v_ref[j & 3] = ref;
+            mbar_arrive(&sm.r_full[j & 3]);
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const int row = 32 * w + 2 * (8 * i + pr) + r;
+#pragma unroll
+                for (int b = 0; b < kBlocks; ++b) {
+                    // four codes of elements 8c .. and four of 8c + 4 ..
+                    const uint32_t x = code[i][r * kWords + (b >> 1)], y = code[i][(2 + r) * kWords + (b >> 1)];
+                    const uint32_t word = __byte_perm(x, y, b & 1 ? 0x7632 : 0x5410);
+                    const uint32_t s2 = operand_scale((scale[i][r] >> (8 * b)) & 0xFFu, ref);
+                    const int chunk = (4 * (b & 1) + c) ^ (row & 7);
+                    *reinterpret_cast<uint4*>(sm.v[stage] + (b >> 1) * 16384 + row * 128 + chunk * 16) = widen_codes(word, s2);
+                }
+            }
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(&sm.v_full[stage]);
+    }
+    cp_async_wait<0>();
+}
+
+// One thread: the matrix products of all units.
+template <int D>
+__device__ __forceinline__ void many_products(const AttendParams& p, ManyShared<D>& sm) {
+    constexpr uint32_t kF32 = 1u << 4;  // fp32 sums, f16 operands
+    constexpr uint32_t kScoreDesc = kF32 | ((128u >> 3) << 17) | ((128u >> 4) << 24);
+    constexpr uint32_t kValueDesc = kF32 | (1u << 16) | (static_cast<uint32_t>(D >> 3) << 17) | ((128u >> 4) << 24);
+    const uint32_t tm = sm.tmem;
+    int j = 0, units = 0;
+    Walk& walk = sm.course[16].walk;
+    Unit& unit = sm.course[16].unit;
+    // O_t (+)= P_t V of block i
+    auto values = [&](int t, int i, bool first) -> bool {
+        if (!mbar_wait(&sm.p_full[t], i & 1, &sm.abort)) return false;
+        if (t == 0 && !mbar_wait(&sm.v_full[i & 1], (i >> 1) & 1, &sm.abort)) return false;
+        tc_fence_after();
+        const uint64_t vd = desc_mn_sw128(smem_u32(sm.v[i & 1]), 16384);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            tc_mma_f16_ts(tm + 256 + 128 * t, tm + 128 * t + 8 * k, vd + static_cast<uint64_t>(k * 2048 >> 4), kValueDesc,
+                          first && k == 0 ? 0u : 1u);
+        return true;
+    };
+    while (walk.next(p, kManyShift, unit)) {
+        for (int block = unit.begin; block < unit.end; ++block, ++j) {
+            if (!mbar_wait(&sm.k_full[j & 1], (j >> 1) & 1, &sm.abort)) return;
+            const bool first = block == unit.begin;
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                if (first) {
+                    if (!mbar_wait(&sm.q_full[t], units & 1, &sm.abort)) return;
+                } else {
+                    if (!values(t, j - 1, block - 1 == unit.begin)) return;
+                    if (t == 1) tc_commit(&sm.v_free[(j - 1) & 1]);
+                }
+                tc_fence_after();
+                const uint64_t qd = desc_sw128(smem_u32(sm.q[t])), kd = desc_sw128(smem_u32(sm.k[j & 1]));
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k) {
+                    const uint64_t at = ((k >> 2) * 16384 + (k & 3) * 32) >> 4;
+                    tc_mma_f16(tm + 128 * t, qd + at, kd + at, kScoreDesc, k ? 1u : 0u);
+                }
+                mbar_arrive(&sm.s_full[t]);  // what this thread has seen (the block's references) goes on with it
+                tc_commit(&sm.s_full[t]);
+            }
+            tc_commit(&sm.k_free[j & 1]);
+        }
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            if (!values(t, j - 1, unit.end - unit.begin == 1)) return;
+            tc_commit(&sm.o_full[t]);
+        }
+        tc_commit(&sm.v_free[(j - 1) & 1]);
+        ++units;
     }
 }
 
-// Joins the parts of a row: one warp per (sequence, query, head).  Rows that one CTA wrote are left alone,
-// rows that see nothing get their zeros here.
+// A thread's query row: what it sees, where its result goes, its score factor; and the row itself to shared
+// memory (zeros for rows past the tile's last).
+struct QueryRow {
+    int lo, hi;
+    int64_t out;  // row of out, or < 0
+    float factor;
+};
+template <int D>
+__device__ __forceinline__ QueryRow load_query(const AttendParams& p, ManyShared<D>& sm, const Unit& u, int t, int tid) {
+    QueryRow q = {0, -1, -1, 1.0f};
+    const int r = 128 * t + tid;
+    uint8_t* dst = sm.q[t] + tid * 128;
+    if (r >= u.t.nrows) {
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i)
+            *reinterpret_cast<uint4*>(dst + (i >> 3) * 16384 + ((i & 7) ^ (tid & 7)) * 16) = make_uint4(0, 0, 0, 0);
+    } else {
+        const int rr = u.t.r0 + r, qi = rr / p.G, h = u.kvh * p.G + rr - qi * p.G;
+        q.hi = u.t.s.pos0 + qi;
+        q.lo = first_key(p, q.hi);
+        q.out = (u.t.s.row0 + qi) * p.Hq + h;
+        const uint4* src = reinterpret_cast<const uint4*>(p.q + (u.t.s.row0 + qi) * p.ldq + static_cast<int64_t>(h) * D);
+        uint4 x[D / 8];
+        uint32_t top = 0;
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) x[i] = src[i];
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) {
+            const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) top = max(top, max(w[k] << 16 & 0x7FFFFFFFu, w[k] & 0x7FFF0000u));
+        }
+        const uint32_t E = query_exponent(top);
+        q.factor = score_factor(p.scale_log2, E);
+        const float mul = query_multiplier(E);
+#pragma unroll
+        for (int b = 0; b < D / 32; ++b) {
+            float2 f[16], m[16];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t w[4] = {x[4 * b + i].x, x[4 * b + i].y, x[4 * b + i].z, x[4 * b + i].w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) f[4 * i + k] = make_float2(bf_lo(w[k]), bf_hi(w[k]));
+            }
+#pragma unroll
+            for (int i = 0; i < 16; ++i) m[i] = make_float2(mul, mul);
+            scale_fwht32(f, m);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                uint32_t h4[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const __half2 y = __floats2half2_rn(f[4 * i + k].x * kHadamardNorm, f[4 * i + k].y * kHadamardNorm);
+                    h4[k] = *reinterpret_cast<const uint32_t*>(&y);
+                }
+                *reinterpret_cast<uint4*>(dst + (b >> 1) * 16384 + ((4 * (b & 1) + i) ^ (tid & 7)) * 16) =
+                    make_uint4(h4[0], h4[1], h4[2], h4[3]);
+            }
+        }
+    }
+    fence_proxy_async_smem();
+    mbar_arrive(&sm.q_full[t]);
+    return q;
+}
+
+template <int D>
+__device__ __forceinline__ void many_softmax(const AttendParams& p, ManyShared<D>& sm, int t, int tid) {
+    const uint32_t lanes = static_cast<uint32_t>(tid & 96) << 16;  // the warp's 32 lanes of tensor memory
+    const uint32_t ts = sm.tmem + 128 * t + lanes, to = sm.tmem + 256 + 128 * t + lanes;
+    int j = 0, units = 0;
+    auto& course = sm.course[4 * t + (tid >> 5)];
+    const Unit& unit = course.unit;
+    bool more = next_unit<D>(p, course, tid & 31);
+    if (!more) return;
+    QueryRow row = load_query<D>(p, sm, unit, t, tid);
+    while (more) {
+        float ref = 0.0f, bound = -INFINITY, sum = 0.0f;
+        int vref = 0;
+        const int begin = unit.begin, end = unit.end;
+        for (int block = begin; block < end; ++block, ++j) {
+            if (!warp_wait(&sm.r_full[j & 3], (j >> 2) & 1, &sm.abort)) return;
+            if (!warp_wait(&sm.s_full[t], j & 1, &sm.abort)) return;
+            tc_fence_after();
+            float s[128];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) tmem_ld32(ts + 32 * i, *reinterpret_cast<uint32_t(*)[32]>(s + 32 * i));
+            float f[4];
+            int gone = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                // score of a product: times 2^(k_ref - 127 - kOperandLift)
+                f[i] = fmaxf(row.factor * __uint_as_float(static_cast<uint32_t>(max(sm.k_ref[j & 3][i] - kOperandLift, 1)) << 23),
+                             1.17549435e-38f);
+                gone |= sm.gone[j & 3][i] << (2 * i);
+            }
+            tmem_ld_wait();
+            const int lo = row.lo - block * 128, hi = row.hi - block * 128;
+            if (__any_sync(0xFFFFFFFFu, gone || lo > 0 || hi < 127)) {
+#pragma unroll
+                for (int i = 0; i < 128; ++i)
+                    if (i < lo || i > hi || ((gone >> (i >> 4)) & 1)) s[i] = -INFINITY;
+            }
+            float m = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float a = fmax3(s[32 * i], s[32 * i + 1], s[32 * i + 2]), z = fmax3(s[32 * i + 16], s[32 * i + 17], s[32 * i + 18]);
+#pragma unroll
+                for (int k = 3; k < 15; k += 2) {
+                    a = fmax3(a, s[32 * i + k], s[32 * i + k + 1]);
+                    z = fmax3(z, s[32 * i + 16 + k], s[32 * i + 16 + k + 1]);
+                }
+                a = fmax3(a, s[32 * i + 15], s[32 * i + 31]);
+                m = fmaxf(m, fmaxf(a, z) * f[i]);
+            }
+            const int nv = sm.v_ref[j & 3];
+            if (__any_sync(0xFFFFFFFFu, m > bound || nv != vref)) {
+                float scale = nv - vref < 127 ? __uint_as_float(static_cast<uint32_t>(127 - (nv - vref)) << 23) : 0.0f;
+                vref = nv;
+                if (m > bound - kSlack) {  // false while the row has seen nothing
+                    const float old = ref;
+                    ref = m - kLift;
+                    const float shift = bound == -INFINITY ? 0.0f : exp2_approx(old - ref);
+                    bound = m + kSlack;
+                    sum *= shift;
+                    scale *= shift;
+                }
+                if (block != begin) {
+#pragma unroll
+                    for (int i = 0; i < D / 16; ++i) {
+                        uint32_t o[16];
+                        tmem_ld16(to + 16 * i, o);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * scale);
+                        tmem_st16(to + 16 * i, o);
+                    }
+                }
+            }
+            float2 add[2] = {};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 f2 = make_float2(f[i], f[i]), r2 = make_float2(-ref, -ref);
+                uint32_t h[16];
+#pragma unroll
+                for (int k = 0; k < 16; ++k) {
+                    float2 e = __ffma2_rn(make_float2(s[32 * i + 2 * k], s[32 * i + 2 * k + 1]), f2, r2);
+                    e = make_float2(exp2_approx(e.x), exp2_approx(e.y));
+                    add[k & 1] = __fadd2_rn(add[k & 1], e);
+                    const __half2 y = __floats2half2_rn(e.x, e.y);
+                    h[k] = *reinterpret_cast<const uint32_t*>(&y);
+                }
+                tmem_st16(ts + 16 * i, h);
+            }
+            sum += (add[0].x + add[0].y) + (add[1].x + add[1].y);
+            tmem_st_wait();
+            tc_fence_before();
+            mbar_arrive(&sm.p_full[t]);
+        }
+        // the next unit's queries (this one's have been used: its last scores are there), then this one's results
+        const int64_t out = row.out, slot = unit.slot;
+        more = next_unit<D>(p, course, tid & 31);
+        if (more) row = load_query<D>(p, sm, unit, t, tid);
+        if (!warp_wait(&sm.o_full[t], units & 1, &sm.abort)) return;
+        ++units;
+        tc_fence_after();
+        const float inv = sum > 0.0f ? 1.0f / sum : sum == 0.0f ? 0.0f : sum;
+        const float vs = vref > kOperandLift ? __uint_as_float(static_cast<uint32_t>(vref - kOperandLift) << 23) : 0.0f;
+        const float m = bound == -INFINITY ? -INFINITY : ref;
+        const int64_t at = slot * kManyRows + 128 * t + tid;
+#pragma unroll
+        for (int b = 0; b < D / 32; ++b) {
+            float2 o[16];
+            tmem_ld32(to + 32 * b, *reinterpret_cast<uint32_t(*)[32]>(o));
+            tmem_ld_wait();
+            const float2 i2 = make_float2(inv, inv), v2 = make_float2(vs, vs);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[i] = __fmul2_rn(__fmul2_rn(o[i], i2), v2);
+            if (out < 0) continue;
+            if (slot >= 0) {
+                float4* dst = reinterpret_cast<float4*>(p.part_o + at * D + 32 * b);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) dst[i] = make_float4(o[2 * i].x, o[2 * i].y, o[2 * i + 1].x, o[2 * i + 1].y);
+            } else {
+                float2 n[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) n[i] = make_float2(kHadamardNorm, kHadamardNorm);
+                scale_fwht32(o, n);
+                uint4* dst = reinterpret_cast<uint4*>(p.out + out * D + 32 * b);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    dst[i] = make_uint4(pack_bf16(o[4 * i].x, o[4 * i].y), pack_bf16(o[4 * i + 1].x, o[4 * i + 1].y),
+                                        pack_bf16(o[4 * i + 2].x, o[4 * i + 2].y), pack_bf16(o[4 * i + 3].x, o[4 * i + 3].y));
+            }
+        }
+        tc_fence_before();
+        if (out >= 0) {
+            if (slot >= 0)
+                p.part_ml[at] = make_float2(m, sum);
+            else if (p.lse)
+                p.lse[out] = sum == 0.0f ? -INFINITY : (m + log2f(sum)) * kLn2;
+        }
+    }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kManyThreads, 1) attend_many_kernel(const __grid_constant__ AttendParams p) {
+    extern __shared__ __align__(1024) uint8_t dynamic_many[];
+    ManyShared<D>& sm = *reinterpret_cast<ManyShared<D>*>(
+        dynamic_many + ((1024 - (smem_u32(dynamic_many) & 1023)) & 1023));
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sm.k_full[i], 128), mbar_init(&sm.k_free[i], 1);
+            mbar_init(&sm.v_full[i], 128), mbar_init(&sm.v_free[i], 1);
+            mbar_init(&sm.q_full[i], 128), mbar_init(&sm.s_full[i], 2);
+            mbar_init(&sm.p_full[i], 128), mbar_init(&sm.o_full[i], 1);
+        }
+        for (int i = 0; i < 4; ++i) mbar_init(&sm.r_full[i], 1);
+        mbar_init(&sm.drained, 1);
+        sm.abort = 0;
+        fence_mbar_init();
+    }
+    if (warp == 16) {
+        tmem_alloc(&sm.tmem, 512);
+        tmem_relinquish();
+    }
+    griddep_launch_dependents();
+    griddep_wait();
+    const Place place = find_place<kManyThreads>(p, kManyShift, blockIdx.x, sm.place);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp < 17 && lane == 0) sm.course[warp].walk = Walk(p, place);
+    __syncwarp();
+    if (warp < 8) {
+        setmaxnreg_inc<kSoftmaxRegs>();
+        many_softmax<D>(p, sm, warp >> 2, threadIdx.x & 127);
+    } else if (warp < 12) {
+        setmaxnreg_dec<kCodeRegs>();
+        many_keys<D>(p, sm, warp - 8, lane);
+    } else if (warp < 16) {
+        setmaxnreg_dec<kCodeRegs>();
+        many_values<D>(p, sm, warp - 12, lane);
+    } else {
+        setmaxnreg_dec<kIssueRegs>();
+        if (warp == 16 && lane == 0) {
+            many_products<D>(p, sm);
+            int gave_up = 0;  // nothing is in flight when tensor memory is given back, whatever happened
+            tc_commit(&sm.drained);
+            mbar_wait(&sm.drained, 0, &gave_up);
+        }
+        __syncwarp();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 16) tmem_dealloc(sm.tmem, 512);
+}
+
+// Joins the parts of the units that were cut: CTA (i, y) looks at the boundary of ranges i and i + 1, and if it is
+// the first one inside a unit, joins that unit's rows y, y + gridDim.y, .. (a warp a row).
 template <int D>
 __global__ void __launch_bounds__(128) attend_join_kernel(const __grid_constant__ AttendParams p, int shift) {
     constexpr int kElems = D / 32;  // of a lane, neighbours
+    __shared__ PlaceShared place;
     griddep_launch_dependents();
     griddep_wait();
     const int lane = threadIdx.x & 31;
-    const int64_t item = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-    const int64_t query = item / p.Hq;
-    const int h = static_cast<int>(item - query * p.Hq);
-    const int b = static_cast<int>(query / p.max_q), qi = static_cast<int>(query % p.max_q);
-    if (b >= p.B) return;
-    int64_t before = 0, total_blocks = 0;
-    for (int x = lane; x < p.B; x += 32) {
-        const int64_t n = sequence_blocks(p, sequence_of(p, x), shift) * p.Hk;
-        total_blocks += n;
-        if (x < b) before += n;
-    }
-#pragma unroll
-    for (int x = 16; x > 0; x >>= 1) {
-        total_blocks += __shfl_xor_sync(0xFFFFFFFFu, total_blocks, x);
-        before += __shfl_xor_sync(0xFFFFFFFFu, before, x);
-    }
-    const Sequence s = sequence_of(p, b);
-    if (qi >= s.nq) return;
-    const int kvh = h / p.G, r = qi * p.G + h - kvh * p.G, rows = s.nq * p.G;
-    int64_t u0 = before + kvh * sequence_blocks(p, s, shift);
-    int r0 = 0, n = blocks_of(span_of(p, s, 0, min(p.tile_rows, rows)), shift);
-    while (r0 + p.tile_rows <= r) {
-        u0 += n;
-        r0 += p.tile_rows;
-        n = blocks_of(span_of(p, s, r0, min(p.tile_rows, rows - r0)), shift);
-    }
-    const int64_t len = cut_length(p, total_blocks, shift);
-    const int64_t c0 = u0 / len, c1 = n ? (u0 + n - 1) / len : c0 - 1;  // the CTAs that hold parts
-    if (c0 == c1) return;
+    const Place c = find_place<128>(p, shift, blockIdx.x + 1, place);
+    if (c.pos >= c.total) return;
+    const Tile t = tile_of(p, c.item, shift);
+    const int per = t.blocks + p.unit_cost;
+    const int kvh = static_cast<int>((c.pos - c.item_pos) / per);
+    const int64_t u0 = c.item_pos + static_cast<int64_t>(kvh) * per + p.unit_cost;  // the unit's first block
+    const int64_t c0 = blockIdx.x;  // the CTA that holds it, if it is a unit to join
+    if (u0 >= c.pos || u0 < c.pos - c.len) return;
+    const int parts = static_cast<int>((u0 + t.blocks - 1) / c.len - c0) + 1;
     // the first part is what its CTA's range ends in (slot 1), the others are what theirs begin with (slot 0)
     const int64_t stride = 2 * p.tile_rows;
-    const int64_t at = c0 * stride + r - r0;
-    auto place = [&](int64_t k) { return at + k * stride + (k == 0 ? p.tile_rows : 0); };
-    const int parts = static_cast<int>(c1 - c0 + 1);
-    float m = -INFINITY;
-    for (int k = lane; k < parts; k += 32) m = fmaxf(m, p.part_ml[place(k)].x);
+    for (int r = blockIdx.y * 4 + (threadIdx.x >> 5); r < t.nrows; r += 4 * gridDim.y) {
+        const int64_t at = c0 * stride + r;
+        auto place_of = [&](int k) { return at + k * stride + (k == 0 ? p.tile_rows : 0); };
+        float m = -INFINITY;
+        for (int k = lane; k < parts; k += 32) m = fmaxf(m, p.part_ml[place_of(k)].x);
 #pragma unroll
-    for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, x));
-    float total = 0.0f, o[kElems] = {};
-    for (int k0 = 0; k0 < parts; k0 += 32) {
-        float w = 0.0f;  // of part k0 + lane
-        if (k0 + lane < parts) {
-            const float2 ml = p.part_ml[place(k0 + lane)];
-            if (ml.x != -INFINITY) w = exp2_approx(ml.x - m) * ml.y;
-        }
-        const int n = min(32, parts - k0);
-#pragma unroll 4
-        for (int k = 0; k < n; ++k) {
-            const float wk = __shfl_sync(0xFFFFFFFFu, w, k);
-            const float* src = p.part_o + place(k0 + k) * D + kElems * lane;
-            total += wk;
-#pragma unroll
-            for (int j = 0; j < kElems; ++j) o[j] += wk == 0.0f ? 0.0f : wk * src[j];
-        }
-    }
-    const float inv = total > 0.0f ? kHadamardNorm / total : total == 0.0f ? 0.0f : total;
-#pragma unroll
-    for (int j = 0; j < kElems; ++j) o[j] *= inv;
-#pragma unroll
-    for (int x = 1; x < kElems; x <<= 1)  // distances inside the lane
-#pragma unroll
-        for (int j = 0; j < kElems; ++j)
-            if ((j & x) == 0) {
-                const float a = o[j], z = o[j + x];
-                o[j] = a + z, o[j + x] = a - z;
+        for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, x));
+        float total = 0.0f, o[kElems] = {};
+        for (int k0 = 0; k0 < parts; k0 += 32) {
+            float w = 0.0f;  // of part k0 + lane
+            if (k0 + lane < parts) {
+                const float2 ml = p.part_ml[place_of(k0 + lane)];
+                if (ml.x != -INFINITY) w = exp2_approx(ml.x - m) * ml.y;
             }
+            const int n = min(32, parts - k0);
+#pragma unroll 4
+            for (int k = 0; k < n; ++k) {
+                const float wk = __shfl_sync(0xFFFFFFFFu, w, k);
+                const float* src = p.part_o + place_of(k0 + k) * D + kElems * lane;
+                total += wk;
 #pragma unroll
-    for (int x = 1; x * kElems < 32; x <<= 1) {
-#pragma unroll
-        for (int j = 0; j < kElems; ++j) {
-            const float y = __shfl_xor_sync(0xFFFFFFFFu, o[j], x);
-            o[j] = lane & x ? y - o[j] : o[j] + y;
+                for (int j = 0; j < kElems; ++j) o[j] += wk == 0.0f ? 0.0f : wk * src[j];
+            }
         }
-    }
-    const int64_t row = (s.row0 + qi) * p.Hq + h;
-    uint16_t* dst = p.out + row * D + kElems * lane;
+        const float inv = total > 0.0f ? kHadamardNorm / total : total == 0.0f ? 0.0f : total;
 #pragma unroll
-    for (int j = 0; j < kElems; j += 2) *reinterpret_cast<uint32_t*>(dst + j) = pack_bf16(o[j], o[j + 1]);
-    if (p.lse && lane == 0) p.lse[row] = total == 0.0f ? -INFINITY : (m + log2f(total)) * kLn2;
+        for (int j = 0; j < kElems; ++j) o[j] *= inv;
+#pragma unroll
+        for (int x = 1; x < kElems; x <<= 1)  // distances inside the lane
+#pragma unroll
+            for (int j = 0; j < kElems; ++j)
+                if ((j & x) == 0) {
+                    const float a = o[j], z = o[j + x];
+                    o[j] = a + z, o[j + x] = a - z;
+                }
+#pragma unroll
+        for (int x = 1; x * kElems < 32; x <<= 1) {
+#pragma unroll
+            for (int j = 0; j < kElems; ++j) {
+                const float y = __shfl_xor_sync(0xFFFFFFFFu, o[j], x);
+                o[j] = lane & x ? y - o[j] : o[j] + y;
+            }
+        }
+        const int qi = (t.r0 + r) / p.G;
+        const int64_t row = (t.s.row0 + qi) * p.Hq + kvh * p.G + (t.r0 + r) - qi * p.G;
+        uint16_t* dst = p.out + row * D + kElems * lane;
+#pragma unroll
+        for (int j = 0; j < kElems; j += 2) *reinterpret_cast<uint32_t*>(dst + j) = pack_bf16(o[j], o[j + 1]);
+        if (p.lse && lane == 0) p.lse[row] = total == 0.0f ? -INFINITY : (m + log2f(total)) * kLn2;
+    }
 }
 
 // ------------------------------------------------------------------------------------ host side
@@ -767,20 +1393,26 @@ __global__ void __launch_bounds__(128) attend_join_kernel(const __grid_constant_
 constexpr int64_t kMaxKeys = int64_t{1} << 30;  // of a sequence: positions and block ends stay in 32 bits
 
 // How a call is split, from what the host knows (not the sequences' lengths).
+constexpr int kFewMost = 64;  // query rows of a unit up to which attend_few_kernel is used
 struct AttendPlan {
-    int tile_rows, row_tiles, ctas;
+    int tile_rows, row_tiles, ctas, unit_cost;
     int64_t units;
     size_t bytes;
 };
 static AttendPlan plan_attend(int64_t B, int Hq, int Hk, int D, int64_t max_q) {
     AttendPlan a;
     const int64_t rows = max_q * (Hq / Hk);
-    a.tile_rows = rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
+    a.tile_rows = rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= kFewMost ? 32 : kManyRows;
     a.row_tiles = static_cast<int>((rows + a.tile_rows - 1) / a.tile_rows);
     a.units = B * Hk * a.row_tiles;
-    // cut while there are few units: many balance themselves, and need no joining
-    const int resident = sm_count() * few_resident(a.tile_rows / 8);
-    a.ctas = a.units >= 4 * resident ? 0 : resident;
+    if (a.tile_rows == kManyRows) {
+        a.ctas = sm_count();
+        a.unit_cost = 2;
+    } else {  // cut while there are few units: many balance themselves, and need no joining
+        const int resident = sm_count() * few_resident(a.tile_rows / 8);
+        a.ctas = a.units >= 4 * resident ? 0 : resident;
+        a.unit_cost = 8;
+    }
     a.bytes = static_cast<size_t>(a.ctas) * 2 * a.tile_rows * (static_cast<size_t>(D) * 4 + 8);
     a.bytes = (a.bytes + 255) / 256 * 256 + 256;
     return a;
@@ -796,16 +1428,29 @@ static int launch_few(const AttendParams& p, unsigned blocks, cudaStream_t strea
 }
 
 template <int D>
+static int launch_many(const AttendParams& p, cudaStream_t stream) {
+    constexpr size_t kSmem = sizeof(ManyShared<D>) + 1024;
+    static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
+    // setmaxnreg.inc takes registers from those the CTA was launched with: with fewer it would wait forever
+    cudaFuncAttributes fa;
+    if (cudaFuncGetAttributes(&fa, attend_many_kernel<D>) != cudaSuccess || fa.numRegs < kManyLaunchRegs) return MACAQ_ECUDA;
+    if (cudaFuncSetAttribute(attend_many_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess)
+        return MACAQ_ECUDA;
+    return launch_dependent_smem(attend_many_kernel<D>, dim3(p.ctas), kManyThreads, kSmem, stream, p);
+}
+
+template <int D>
 static int launch_attend(const AttendParams& p, int64_t units, cudaStream_t stream) {
     const int64_t blocks = p.ctas ? p.ctas : units;
-    const int64_t join = (static_cast<int64_t>(p.B) * p.max_q * p.Hq + 3) / 4;
-    if (blocks > kMaxDim || join > kMaxDim) return MACAQ_ESHAPE;
+    if (blocks > kMaxDim) return MACAQ_ESHAPE;
     const auto n = static_cast<unsigned>(blocks);
-    const int st = p.tile_rows == 8    ? launch_few<D, 1>(p, n, stream)
+    const int st = p.tile_rows == kManyRows ? launch_many<D>(p, stream)
+                   : p.tile_rows == 8  ? launch_few<D, 1>(p, n, stream)
                    : p.tile_rows == 16 ? launch_few<D, 2>(p, n, stream)
                                        : launch_few<D, 4>(p, n, stream);
-    if (st != MACAQ_OK || !p.ctas) return st;
-    return launch_dependent(attend_join_kernel<D>, dim3(static_cast<unsigned>(join)), 128, stream, p, kFewShift);
+    if (st != MACAQ_OK || p.ctas < 2) return st;
+    return launch_dependent(attend_join_kernel<D>, dim3(p.ctas - 1, p.tile_rows / 8), 128, stream, p,
+                            p.tile_rows == kManyRows ? kManyShift : kFewShift);
 }
 
 }  // namespace macaq
@@ -844,6 +1489,7 @@ extern "C" int macaq_kv4_attention(const uint16_t* q, int64_t T, int64_t ldq, in
     p.kv_lens = kv_lens, p.cu_q = cu_q, p.B = static_cast<int>(B), p.max_q = static_cast<int>(max_q);
     p.scale_log2 = scale * kLog2e, p.window = static_cast<int>(window < kMaxDim ? window : 0), p.out = out, p.lse = lse;
     p.tile_rows = plan.tile_rows, p.row_tiles = plan.row_tiles, p.ctas = plan.ctas;
+    p.unit_cost = plan.unit_cost;
     p.part_ml = static_cast<float2*>(workspace);
     p.part_o = reinterpret_cast<float*>(p.part_ml + static_cast<int64_t>(p.ctas) * 2 * p.tile_rows);
     const auto s = static_cast<cudaStream_t>(stream);
