@@ -710,6 +710,7 @@ __global__ void __launch_bounds__(kFewThreads, few_resident(NT)) attend_few_kern
 //                    the rows' queries (transform, f16, shared memory), after it the results
 //   warpgroup 2      K: codes to f16 in shared memory, K-major
 //   warpgroup 3      V: likewise, elements along the rows (MN-major, as V's codes lie)
+//   warp 17          finds the CTA's units
 //   warp 16          issues S_t = Q_t K^T and O_t += P_t V (tcgen05, f16 operands, fp32 sums)
 // so the two tiles' matrix products and exponentials alternate, and the codes of the next blocks are widened
 // meanwhile.  In tensor memory stand S_0, S_1 (each 128 columns, its first 64 then P) and O_0, O_1.
@@ -719,10 +720,11 @@ __global__ void __launch_bounds__(kFewThreads, few_resident(NT)) attend_few_kern
 constexpr int kManyShift = 7;
 constexpr int kManyRows = 256;
 constexpr int kManyThreads = 640;
-// Registers of a thread: 96 at launch (640 threads), then split 160 / 64 / 32 (softmax / codes / products).
-constexpr int kManyLaunchRegs = 96, kSoftmaxRegs = 160, kCodeRegs = 64, kIssueRegs = 32;
+// Registers of a thread: 96 at launch (640 threads), then split 144 / 72 / 48 (softmax / codes / products).
+constexpr int kManyLaunchRegs = 96, kSoftmaxRegs = 144, kCodeRegs = 72, kIssueRegs = 48;
 static_assert(2 * kSoftmaxRegs + 2 * kCodeRegs + kIssueRegs <= 5 * kManyLaunchRegs, "registers of a CTA");
 constexpr int kOperandLift = 12;
+constexpr int kManyUnits = 4;
 
 template <int D>
 struct ManyShared {
@@ -740,26 +742,44 @@ struct ManyShared {
     int abort;
     uint32_t tmem;
     PlaceShared place;
-    // each warp's walk through the CTA's units, kept here to spare registers
-    struct Course {
-        Walk walk;
-        Unit unit;
-    } course[17];
+    // the CTA's units in order, written by one warp (so that no other spends registers on finding them) and read
+    // by the 17 that work on them; past the last one stands an empty one
+    Unit unit[kManyUnits];
+    uint64_t unit_full[kManyUnits], unit_free[kManyUnits];
 };
-
-// The warp's next unit.
-template <int D>
-__device__ __forceinline__ bool next_unit(const AttendParams& p, typename ManyShared<D>::Course& c, int lane) {
-    bool more = false;
-    __syncwarp();
-    if (lane == 0) more = c.walk.next(p, kManyShift, c.unit);
-    return __shfl_sync(0xFFFFFFFFu, more, 0);
-}
 
 // mbar_wait with one answer for the whole warp.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int* abort) {
+    if (__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity))) return true;
     const bool ok = mbar_wait(bar, parity, abort);
     return __all_sync(0xFFFFFFFFu, ok);
+}
+
+// A warp's next unit: waits for number n, and gives number n - 1 back first.  False: there is none.
+template <int D>
+__device__ __forceinline__ bool next_unit(ManyShared<D>& sm, int n, int lane) {
+    __syncwarp();
+    if (n > 0 && lane == 0) mbar_arrive(&sm.unit_free[(n - 1) % kManyUnits]);
+    if (!warp_wait(&sm.unit_full[n % kManyUnits], (n / kManyUnits) & 1, &sm.abort)) return false;
+    return sm.unit[n % kManyUnits].end > 0;
+}
+
+// One warp: writes the units.
+template <int D>
+__device__ __forceinline__ void many_units(const AttendParams& p, ManyShared<D>& sm, const Place& place, int lane) {
+    Walk walk(p, place);
+    bool more = true;
+    for (int n = 0; more; ++n) {
+        const int at = n % kManyUnits;
+        if (n >= kManyUnits && !warp_wait(&sm.unit_free[at], ((n / kManyUnits) & 1) ^ 1, &sm.abort)) return;
+        Unit u;
+        more = walk.next(p, kManyShift, u);
+        if (!more) u.end = 0;
+        if (lane == 0) {
+            sm.unit[at] = u;
+            mbar_arrive(&sm.unit_full[at]);
+        }
+    }
 }
 
 __device__ __forceinline__ void group_sync(int id) { asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory"); }
@@ -770,8 +790,8 @@ template <int D, bool IS_V>
 struct CodeStream {
     static constexpr int kBlocks = D / 32;
     const AttendParams& p;
-    typename ManyShared<D>::Course& course;
-    const Unit& unit;
+    ManyShared<D>& sm;
+    int n = 0;  // units begun
     bool more;
     int block;        // of the request after the pending one
     int32_t page[2];  // its pages (of its first and second 16 tokens)
@@ -780,32 +800,38 @@ struct CodeStream {
     int first, last;  // the tokens of the pending request that any row sees, relative to its first
     int w, lane;
 
-    __device__ __forceinline__ CodeStream(const AttendParams& p_, typename ManyShared<D>::Course& c, int w_, int lane_)
-        : p(p_), course(c), unit(c.unit), w(w_), lane(lane_) {
-        more = next_unit<D>(p, course, lane);
-        if (more) block = unit.begin;
+    __device__ __forceinline__ CodeStream(const AttendParams& p_, ManyShared<D>& sm_, int w_, int lane_)
+        : p(p_), sm(sm_), w(w_), lane(lane_) {
+        begin_unit();
         look();
+    }
+    __device__ __forceinline__ const Unit& unit() const { return sm.unit[(n - 1) % kManyUnits]; }
+    __device__ __forceinline__ void begin_unit() {
+        more = next_unit<D>(sm, n++, lane);
+        if (more) block = unit().begin;
     }
     __device__ __forceinline__ void look() {
         page[0] = page[1] = -1;
         if (!more) return;
+        const Unit& u0 = unit();
         const int t = block * 128 + 32 * w;
-        const int32_t* table = p.tables + unit.t.b * p.table_width;
+        const int32_t* table = p.tables + u0.t.b * p.table_width;
 #pragma unroll
         for (int u = 0; u < 2; ++u)
-            if (t + 16 * u <= unit.t.sp.last_hi && t + 16 * u + 15 >= unit.t.sp.first_lo)
+            if (t + 16 * u <= u0.t.sp.last_hi && t + 16 * u + 15 >= u0.t.sp.first_lo)
                 page[u] = table[(t + 16 * u) >> p.page_shift];
     }
     // Starts the copies of the next block and looks further.
     __device__ __forceinline__ void request(uint8_t* raw) {
         if (more) {
+            const Unit& u0 = unit();
             const int t0 = block * 128 + 32 * w;
             const PageLayout<D> lay{p.page_size};
             there = seen = 0;
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
                 const int t = t0 + 16 * u;
-                if (t > unit.t.sp.last_hi || t + 15 < unit.t.sp.first_lo) continue;
+                if (t > u0.t.sp.last_hi || t + 15 < u0.t.sp.first_lo) continue;
                 seen |= 1u << u;
                 if (static_cast<unsigned>(page[u]) >= static_cast<uint64_t>(p.num_pages)) {
                     if (lane == 0) report_index();
@@ -813,7 +839,7 @@ struct CodeStream {
                 }
                 there |= 1u << u;
                 const int at = t & (p.page_size - 1);
-                const uint8_t* src = p.cache + (static_cast<int64_t>(page[u]) * p.Hk + unit.kvh) * lay.bytes();
+                const uint8_t* src = p.cache + (static_cast<int64_t>(page[u]) * p.Hk + u0.kvh) * lay.bytes();
                 const uint8_t* codes = src + (IS_V ? lay.v_codes() : 0) + at * lay.kRow + 16 * lane;
 #pragma unroll
                 for (int x = 0; x < D / 64; ++x) {
@@ -827,11 +853,8 @@ struct CodeStream {
                     cp_async16(smem_u32(raw) + 16 * D + 16 * kBlocks * u + 16 * lane,
                                src + (IS_V ? lay.v_scales() : lay.k_scales()) + at * kBlocks + 16 * lane);
             }
-            first = unit.t.sp.first_lo - t0, last = unit.t.sp.last_hi - t0;
-            if (++block == unit.end) {
-                more = next_unit<D>(p, course, lane);
-                if (more) block = unit.begin;
-            }
+            first = u0.t.sp.first_lo - t0, last = u0.t.sp.last_hi - t0;
+            if (++block == u0.end) begin_unit();
             look();
         }
         cp_async_commit();
@@ -862,7 +885,7 @@ template <int D>
 __device__ __forceinline__ void many_keys(const AttendParams& p, ManyShared<D>& sm, int w, int lane) {
     constexpr int kBlocks = D / 32;
     uint8_t* raw = sm.raw[w];
-    CodeStream<D, false> cs(p, sm.course[8 + w], w, lane);
+    CodeStream<D, false> cs(p, sm, w, lane);
     bool pending = cs.more;
     cs.request(raw);
     // lane (token, chunk c of 8 elements a block): 8 tokens a step; the tokens of 8 neighbouring lanes differ by 4,
@@ -921,7 +944,7 @@ template <int D>
 __device__ __forceinline__ void many_values(const AttendParams& p, ManyShared<D>& sm, int w, int lane) {
     constexpr int kBlocks = D / 32, kWords = kBlocks / 2;
     uint8_t* raw = sm.raw[4 + w];
-    CodeStream<D, true> cs(p, sm.course[12 + w], w, lane);
+    CodeStream<D, true> cs(p, sm, w, lane);
     bool pending = cs.more;
     cs.request(raw);
     // lane (pair of tokens, elements 8c .. 8c + 7 of each block): 8 pairs a step; 8 neighbouring lanes are 4 pairs
@@ -1001,58 +1024,69 @@ __device__ __forceinline__ void many_values(const AttendParams& p, ManyShared<D>
     cp_async_wait<0>();
 }
 
-// One thread: the matrix products of all units.
+// One warp: the matrix products of all units, issued by one of its lanes.
 template <int D>
-__device__ __forceinline__ void many_products(const AttendParams& p, ManyShared<D>& sm) {
+__device__ __forceinline__ void many_products(ManyShared<D>& sm, int lane) {
     constexpr uint32_t kF32 = 1u << 4;  // fp32 sums, f16 operands
     constexpr uint32_t kScoreDesc = kF32 | ((128u >> 3) << 17) | ((128u >> 4) << 24);
     constexpr uint32_t kValueDesc = kF32 | (1u << 16) | (static_cast<uint32_t>(D >> 3) << 17) | ((128u >> 4) << 24);
     const uint32_t tm = sm.tmem;
+    const uint64_t q0 = desc_sw128(smem_u32(sm.q[0])), k0 = desc_sw128(smem_u32(sm.k[0]));
+    const uint64_t v0 = desc_mn_sw128(smem_u32(sm.v[0]), 16384);
+    constexpr uint32_t kNext = ManyShared<D>::kTile >> 4;
     int j = 0, units = 0;
-    Walk& walk = sm.course[16].walk;
-    Unit& unit = sm.course[16].unit;
     // O_t (+)= P_t V of block i
     auto values = [&](int t, int i, bool first) -> bool {
-        if (!mbar_wait(&sm.p_full[t], i & 1, &sm.abort)) return false;
-        if (t == 0 && !mbar_wait(&sm.v_full[i & 1], (i >> 1) & 1, &sm.abort)) return false;
+        if (!warp_wait(&sm.p_full[t], i & 1, &sm.abort)) return false;
+        if (t == 0 && !warp_wait(&sm.v_full[i & 1], (i >> 1) & 1, &sm.abort)) return false;
         tc_fence_after();
-        const uint64_t vd = desc_mn_sw128(smem_u32(sm.v[i & 1]), 16384);
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-            tc_mma_f16_ts(tm + 256 + 128 * t, tm + 128 * t + 8 * k, vd + static_cast<uint64_t>(k * 2048 >> 4), kValueDesc,
-                          first && k == 0 ? 0u : 1u);
+        const uint64_t vd = v0 + (i & 1) * kNext;
+        if (elect_one()) {
+#pragma unroll 2
+            for (int k = 0; k < 8; ++k)
+                tc_mma_f16_ts(tm + 256 + 128 * t, tm + 128 * t + 8 * k, vd + (k * 2048 >> 4), kValueDesc,
+                              first && k == 0 ? 0u : 1u);
+        }
+        __syncwarp();
         return true;
     };
-    while (walk.next(p, kManyShift, unit)) {
-        for (int block = unit.begin; block < unit.end; ++block, ++j) {
-            if (!mbar_wait(&sm.k_full[j & 1], (j >> 1) & 1, &sm.abort)) return;
-            const bool first = block == unit.begin;
+    while (next_unit<D>(sm, units, lane)) {
+        const Unit& unit = sm.unit[units % kManyUnits];
+        const int n = unit.end - unit.begin;
+        for (int i = 0; i < n; ++i, ++j) {
+            if (!warp_wait(&sm.k_full[j & 1], (j >> 1) & 1, &sm.abort)) return;
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
-                if (first) {
-                    if (!mbar_wait(&sm.q_full[t], units & 1, &sm.abort)) return;
-                } else {
-                    if (!values(t, j - 1, block - 1 == unit.begin)) return;
-                    if (t == 1) tc_commit(&sm.v_free[(j - 1) & 1]);
+                if (i == 0) {
+                    if (!warp_wait(&sm.q_full[t], units & 1, &sm.abort)) return;
+                } else if (!values(t, j - 1, i == 1)) {
+                    return;
                 }
                 tc_fence_after();
-                const uint64_t qd = desc_sw128(smem_u32(sm.q[t])), kd = desc_sw128(smem_u32(sm.k[j & 1]));
-#pragma unroll
-                for (int k = 0; k < D / 16; ++k) {
-                    const uint64_t at = ((k >> 2) * 16384 + (k & 3) * 32) >> 4;
-                    tc_mma_f16(tm + 128 * t, qd + at, kd + at, kScoreDesc, k ? 1u : 0u);
+                const uint64_t qd = q0 + t * kNext, kd = k0 + (j & 1) * kNext;
+                if (elect_one()) {
+                    if (t == 1 && i != 0) tc_commit(&sm.v_free[(j - 1) & 1]);
+#pragma unroll 4
+                    for (int k = 0; k < D / 16; ++k) {
+                        const uint32_t at = ((k >> 2) * 16384 + (k & 3) * 32) >> 4;
+                        tc_mma_f16(tm + 128 * t, qd + at, kd + at, kScoreDesc, k ? 1u : 0u);
+                    }
+                    mbar_arrive(&sm.s_full[t]);  // what this thread has seen (the block's references) goes on with it
+                    tc_commit(&sm.s_full[t]);
+                    if (t == 1) tc_commit(&sm.k_free[j & 1]);
                 }
-                mbar_arrive(&sm.s_full[t]);  // what this thread has seen (the block's references) goes on with it
-                tc_commit(&sm.s_full[t]);
+                __syncwarp();
             }
-            tc_commit(&sm.k_free[j & 1]);
         }
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-            if (!values(t, j - 1, unit.end - unit.begin == 1)) return;
-            tc_commit(&sm.o_full[t]);
+            if (!values(t, j - 1, n == 1)) return;
+            if (elect_one()) {
+                tc_commit(&sm.o_full[t]);
+                if (t == 1) tc_commit(&sm.v_free[(j - 1) & 1]);
+            }
+            __syncwarp();
         }
-        tc_commit(&sm.v_free[(j - 1) & 1]);
         ++units;
     }
 }
@@ -1127,12 +1161,11 @@ __device__ __forceinline__ void many_softmax(const AttendParams& p, ManyShared<D
     const uint32_t lanes = static_cast<uint32_t>(tid & 96) << 16;  // the warp's 32 lanes of tensor memory
     const uint32_t ts = sm.tmem + 128 * t + lanes, to = sm.tmem + 256 + 128 * t + lanes;
     int j = 0, units = 0;
-    auto& course = sm.course[4 * t + (tid >> 5)];
-    const Unit& unit = course.unit;
-    bool more = next_unit<D>(p, course, tid & 31);
+    bool more = next_unit<D>(sm, 0, tid & 31);
     if (!more) return;
-    QueryRow row = load_query<D>(p, sm, unit, t, tid);
+    QueryRow row = load_query<D>(p, sm, sm.unit[0], t, tid);
     while (more) {
+        const Unit& unit = sm.unit[units % kManyUnits];
         float ref = 0.0f, bound = -INFINITY, sum = 0.0f;
         int vref = 0;
         const int begin = unit.begin, end = unit.end;
@@ -1140,28 +1173,32 @@ __device__ __forceinline__ void many_softmax(const AttendParams& p, ManyShared<D
             if (!warp_wait(&sm.r_full[j & 3], (j >> 2) & 1, &sm.abort)) return;
             if (!warp_wait(&sm.s_full[t], j & 1, &sm.abort)) return;
             tc_fence_after();
+            // The first 64 scores stay in registers, the others are read once for the maximum and again for their
+            // weights (which are written over the first 64 columns).
             float s[128];
 #pragma unroll
             for (int i = 0; i < 4; ++i) tmem_ld32(ts + 32 * i, *reinterpret_cast<uint32_t(*)[32]>(s + 32 * i));
             float f[4];
-            int gone = 0;
+            uint32_t gone = 0;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 // score of a product: times 2^(k_ref - 127 - kOperandLift)
                 f[i] = fmaxf(row.factor * __uint_as_float(static_cast<uint32_t>(max(sm.k_ref[j & 3][i] - kOperandLift, 1)) << 23),
                              1.17549435e-38f);
-                gone |= sm.gone[j & 3][i] << (2 * i);
+                gone |= static_cast<uint32_t>(sm.gone[j & 3][i]) << (2 * i);
             }
             tmem_ld_wait();
             const int lo = row.lo - block * 128, hi = row.hi - block * 128;
-            if (__any_sync(0xFFFFFFFFu, gone || lo > 0 || hi < 127)) {
+            const bool masked = __any_sync(0xFFFFFFFFu, gone != 0 || lo > 0 || hi < 127);
+            auto mask = [&](int i) {  // columns 32 i .. 32 i + 31
 #pragma unroll
-                for (int i = 0; i < 128; ++i)
-                    if (i < lo || i > hi || ((gone >> (i >> 4)) & 1)) s[i] = -INFINITY;
-            }
+                for (int k = 32 * i; k < 32 * i + 32; ++k)
+                    if (k < lo || k > hi || ((gone >> (k >> 4)) & 1)) s[k] = -INFINITY;
+            };
             float m = -INFINITY;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
+                if (masked) mask(i);
                 float a = fmax3(s[32 * i], s[32 * i + 1], s[32 * i + 2]), z = fmax3(s[32 * i + 16], s[32 * i + 17], s[32 * i + 18]);
 #pragma unroll
                 for (int k = 3; k < 15; k += 2) {
@@ -1198,6 +1235,16 @@ __device__ __forceinline__ void many_softmax(const AttendParams& p, ManyShared<D
             float2 add[2] = {};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
+                if (i == 1) tmem_ld32(ts + 64, *reinterpret_cast<uint32_t(*)[32]>(s + 64));
+                if (i == 2) {
+                    tmem_ld_wait();
+                    tmem_ld32(ts + 96, *reinterpret_cast<uint32_t(*)[32]>(s + 96));
+                    if (masked) mask(2);
+                }
+                if (i == 3) {
+                    tmem_ld_wait();
+                    if (masked) mask(3);
+                }
                 const float2 f2 = make_float2(f[i], f[i]), r2 = make_float2(-ref, -ref);
                 uint32_t h[16];
 #pragma unroll
@@ -1217,8 +1264,8 @@ __device__ __forceinline__ void many_softmax(const AttendParams& p, ManyShared<D
         }
         // the next unit's queries (this one's have been used: its last scores are there), then this one's results
         const int64_t out = row.out, slot = unit.slot;
-        more = next_unit<D>(p, course, tid & 31);
-        if (more) row = load_query<D>(p, sm, unit, t, tid);
+        more = next_unit<D>(sm, units + 1, tid & 31);
+        if (more) row = load_query<D>(p, sm, sm.unit[(units + 1) % kManyUnits], t, tid);
         if (!warp_wait(&sm.o_full[t], units & 1, &sm.abort)) return;
         ++units;
         tc_fence_after();
@@ -1276,6 +1323,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) attend_many_kernel(const __gr
         }
         for (int i = 0; i < 4; ++i) mbar_init(&sm.r_full[i], 1);
         mbar_init(&sm.drained, 1);
+        for (int i = 0; i < kManyUnits; ++i) mbar_init(&sm.unit_full[i], 1), mbar_init(&sm.unit_free[i], 17);
         sm.abort = 0;
         fence_mbar_init();
     }
@@ -1289,8 +1337,6 @@ __global__ void __launch_bounds__(kManyThreads, 1) attend_many_kernel(const __gr
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp < 17 && lane == 0) sm.course[warp].walk = Walk(p, place);
-    __syncwarp();
     if (warp < 8) {
         setmaxnreg_inc<kSoftmaxRegs>();
         many_softmax<D>(p, sm, warp >> 2, threadIdx.x & 127);
@@ -1302,11 +1348,15 @@ __global__ void __launch_bounds__(kManyThreads, 1) attend_many_kernel(const __gr
         many_values<D>(p, sm, warp - 12, lane);
     } else {
         setmaxnreg_dec<kIssueRegs>();
-        if (warp == 16 && lane == 0) {
-            many_products<D>(p, sm);
-            int gave_up = 0;  // nothing is in flight when tensor memory is given back, whatever happened
-            tc_commit(&sm.drained);
-            mbar_wait(&sm.drained, 0, &gave_up);
+        if (warp == 17) many_units<D>(p, sm, place, lane);
+        if (warp == 16) {
+            many_products<D>(sm, lane);
+            __syncwarp();
+            if (elect_one()) {
+                int gave_up = 0;  // nothing is in flight when tensor memory is given back, whatever happened
+                tc_commit(&sm.drained);
+                mbar_wait(&sm.drained, 0, &gave_up);
+            }
         }
         __syncwarp();
     }

@@ -259,6 +259,14 @@ __device__ __forceinline__ void tc_mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, 
         : "memory");
 }
 
+// True in one lane of a converged warp, always the same one; the compiler then knows that what follows runs in
+// one thread, and keeps the operands of tcgen05 instructions in uniform registers.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok));
+    return ok != 0;
+}
+
 // Arrive once on `bar` when all previously issued tcgen05 operations of this thread finish.
 __device__ __forceinline__ void tc_commit(uint64_t* bar) {
     asm volatile(
