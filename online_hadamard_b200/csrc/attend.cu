@@ -94,7 +94,7 @@ struct Tile {  // of a sequence; nrows <= 0: none
 };
 __device__ __forceinline__ Tile tile_of(const AttendParams& p, int64_t item, int shift) {
     Tile t;
-    t.b = static_cast<int>(p.row_tiles == 1 ? item : item / p.row_tiles);
+    t.b = static_cast<int>(static_cast<uint32_t>(item) / static_cast<uint32_t>(p.row_tiles));  // fewer than 2^31 tiles
     t.r0 = static_cast<int>(item - static_cast<int64_t>(t.b) * p.row_tiles) * p.tile_rows;
     t.s = sequence_of(p, t.b);
     t.nrows = min(p.tile_rows, t.s.nq * p.G - t.r0);
@@ -129,6 +129,7 @@ __device__ __forceinline__ Place find_place(const AttendParams& p, int shift, in
     const int64_t items = static_cast<int64_t>(p.B) * p.row_tiles, share = (items + THREADS - 1) / THREADS;
     const int64_t a = min(items, threadIdx.x * share), z = min(items, a + share);
     int64_t mine = 0;
+#pragma unroll 1
     for (int64_t x = a; x < z; ++x) mine += tile_places(p, tile_of(p, x, shift));
     int64_t upto = mine;
 #pragma unroll
@@ -150,6 +151,7 @@ __device__ __forceinline__ Place find_place(const AttendParams& p, int shift, in
     c.pos = i * c.len;
     if (c.pos < upto && c.pos >= upto - mine) {
         int64_t at = upto - mine;
+#pragma unroll 1
         for (int64_t x = a; x < z; ++x) {
             const int64_t n = tile_places(p, tile_of(p, x, shift));
             if (c.pos < at + n) {
@@ -175,7 +177,7 @@ struct Walk {
     Walk() = default;
     __device__ __forceinline__ Walk(const AttendParams& p, const Place& c)
         : pos(c.pos), end(c.pos + c.len < c.total ? c.pos + c.len : c.total), item(c.item), item_pos(c.item_pos) {}
-    __device__ __forceinline__ Walk(int64_t unit, int Hk) : pos(unit % Hk), end(-1), item(unit / Hk), item_pos(0) {}
+    __device__ __forceinline__ Walk(uint32_t unit, uint32_t Hk) : pos(unit % Hk), end(-1), item(unit / Hk), item_pos(0) {}
     __device__ __forceinline__ bool next(const AttendParams& p, int shift, Unit& u) {
         if (!p.ctas) {  // one unit
             if (end == 0) return false;
@@ -735,6 +737,7 @@ struct ManyShared {
     alignas(1024) uint8_t v[2][kTile];
     alignas(16) uint8_t raw[8][kRaw];
     uint64_t k_full[2], k_free[2], v_full[2], v_free[2], q_full[2], s_full[2], p_full[2], o_full[2], r_full[4], drained;
+    uint64_t turn[2][4];  // [t][w]: warp w of tile t may take its exponentials
     // of block j at [j % 4]: each K warp's largest scale and its strips (16 tokens) whose page is not there,
     // and V's reference; a slot is rewritten after the products of block j + 2, whose softmax follows that of j.  r_full: V's is there
     int k_ref[4][4], gone[4][4], v_ref[4];
@@ -1112,31 +1115,25 @@ __device__ __forceinline__ QueryRow load_query(const AttendParams& p, ManyShared
         q.hi = u.t.s.pos0 + qi;
         q.lo = first_key(p, q.hi);
         q.out = (u.t.s.row0 + qi) * p.Hq + h;
-        const uint4* src = reinterpret_cast<const uint4*>(p.q + (u.t.s.row0 + qi) * p.ldq + static_cast<int64_t>(h) * D);
-        uint4 x[D / 8];
+        const uint16_t* src = p.q + (u.t.s.row0 + qi) * p.ldq + static_cast<int64_t>(h) * D;
         uint32_t top = 0;
+#pragma unroll 1
+        for (int b = 0; b < D / 32; ++b) {
+            uint32_t w[16];
+            load32(src + 32 * b, w);
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i) x[i] = src[i];
-#pragma unroll
-        for (int i = 0; i < D / 8; ++i) {
-            const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-#pragma unroll
-            for (int k = 0; k < 4; ++k) top = max(top, max(w[k] << 16 & 0x7FFFFFFFu, w[k] & 0x7FFF0000u));
+            for (int k = 0; k < 16; ++k) top = max(top, max(w[k] << 16 & 0x7FFFFFFFu, w[k] & 0x7FFF0000u));
         }
         const uint32_t E = query_exponent(top);
         q.factor = score_factor(p.scale_log2, E);
         const float mul = query_multiplier(E);
-#pragma unroll
+#pragma unroll 1
         for (int b = 0; b < D / 32; ++b) {
+            uint32_t w[16];
+            load32(src + 32 * b, w);
             float2 f[16], m[16];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint32_t w[4] = {x[4 * b + i].x, x[4 * b + i].y, x[4 * b + i].z, x[4 * b + i].w};
-#pragma unroll
-                for (int k = 0; k < 4; ++k) f[4 * i + k] = make_float2(bf_lo(w[k]), bf_hi(w[k]));
-            }
-#pragma unroll
-            for (int i = 0; i < 16; ++i) m[i] = make_float2(mul, mul);
+            for (int k = 0; k < 16; ++k) f[k] = make_float2(bf_lo(w[k]), bf_hi(w[k])), m[k] = make_float2(mul, mul);
             scale_fwht32(f, m);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -1173,11 +1170,6 @@ __device__ __forceinline__ void many_softmax(const AttendParams& p, ManyShared<D
             if (!warp_wait(&sm.r_full[j & 3], (j >> 2) & 1, &sm.abort)) return;
             if (!warp_wait(&sm.s_full[t], j & 1, &sm.abort)) return;
             tc_fence_after();
-            // The first 64 scores stay in registers, the others are read once for the maximum and again for their
-            // weights (which are written over the first 64 columns).
-            float s[128];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) tmem_ld32(ts + 32 * i, *reinterpret_cast<uint32_t(*)[32]>(s + 32 * i));
             float f[4];
             uint32_t gone = 0;
 #pragma unroll
@@ -1187,18 +1179,33 @@ __device__ __forceinline__ void many_softmax(const AttendParams& p, ManyShared<D
                              1.17549435e-38f);
                 gone |= static_cast<uint32_t>(sm.gone[j & 3][i]) << (2 * i);
             }
-            tmem_ld_wait();
             const int lo = row.lo - block * 128, hi = row.hi - block * 128;
-            const bool masked = __any_sync(0xFFFFFFFFu, gone != 0 || lo > 0 || hi < 127);
-            auto mask = [&](int i) {  // columns 32 i .. 32 i + 31
+            if (__any_sync(0xFFFFFFFFu, gone != 0 || lo > 0 || hi < 127)) {  // masked in place
+#pragma unroll 1
+                for (int i = 0; i < 4; ++i) {
+                    uint32_t x[32];
+                    tmem_ld32(ts + 32 * i, x);
+                    // columns lo .. hi, without those whose page is not there
+                    const int a = max(lo - 32 * i, 0), z = min(hi - 32 * i, 31);
+                    uint32_t keep = a > z ? 0u : (0xFFFFFFFFu << a) & (0xFFFFFFFFu >> (31 - z));
+                    keep &= ~(((gone >> (2 * i)) & 1 ? 0xFFFFu : 0u) | ((gone >> (2 * i)) & 2 ? 0xFFFF0000u : 0u));
+                    tmem_ld_wait();
 #pragma unroll
-                for (int k = 32 * i; k < 32 * i + 32; ++k)
-                    if (k < lo || k > hi || ((gone >> (k >> 4)) & 1)) s[k] = -INFINITY;
-            };
+                    for (int k = 0; k < 32; ++k) x[k] = (keep >> k) & 1 ? x[k] : 0xFF800000u;
+                    tmem_st16(ts + 32 * i, x);
+                    tmem_st16(ts + 32 * i + 16, x + 16);
+                }
+                tmem_st_wait();
+            }
+            // The first 64 scores stay in registers, the others are read once for the maximum and again for their
+            // weights (which are written over the first 64 columns).
+            float s[128];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) tmem_ld32(ts + 32 * i, *reinterpret_cast<uint32_t(*)[32]>(s + 32 * i));
+            tmem_ld_wait();
             float m = -INFINITY;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                if (masked) mask(i);
                 float a = fmax3(s[32 * i], s[32 * i + 1], s[32 * i + 2]), z = fmax3(s[32 * i + 16], s[32 * i + 17], s[32 * i + 18]);
 #pragma unroll
                 for (int k = 3; k < 15; k += 2) {
@@ -1221,7 +1228,7 @@ __device__ __forceinline__ void many_softmax(const AttendParams& p, ManyShared<D
                     scale *= shift;
                 }
                 if (block != begin) {
-#pragma unroll
+#pragma unroll 1
                     for (int i = 0; i < D / 16; ++i) {
                         uint32_t o[16];
                         tmem_ld16(to + 16 * i, o);
@@ -1232,6 +1239,11 @@ __device__ __forceinline__ void many_softmax(const AttendParams& p, ManyShared<D
                     }
                 }
             }
+            // The exponentials of the two warps on one scheduler go in turn: together both would take twice as long, and
+            // then both wait for the products; in turn one's exponentials run beside the other's products.
+            if (t == 1 || j > 0) {
+                if (!warp_wait(&sm.turn[t][(tid >> 5) & 3], (t == 1 ? j : j - 1) & 1, &sm.abort)) return;
+            }
             float2 add[2] = {};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -1239,12 +1251,8 @@ __device__ __forceinline__ void many_softmax(const AttendParams& p, ManyShared<D
                 if (i == 2) {
                     tmem_ld_wait();
                     tmem_ld32(ts + 96, *reinterpret_cast<uint32_t(*)[32]>(s + 96));
-                    if (masked) mask(2);
                 }
-                if (i == 3) {
-                    tmem_ld_wait();
-                    if (masked) mask(3);
-                }
+                if (i == 3) tmem_ld_wait();
                 const float2 f2 = make_float2(f[i], f[i]), r2 = make_float2(-ref, -ref);
                 uint32_t h[16];
 #pragma unroll
@@ -1257,6 +1265,7 @@ __device__ __forceinline__ void many_softmax(const AttendParams& p, ManyShared<D
                 }
                 tmem_st16(ts + 16 * i, h);
             }
+            if ((tid & 31) == 0) mbar_arrive(&sm.turn[t ^ 1][(tid >> 5) & 3]);
             sum += (add[0].x + add[0].y) + (add[1].x + add[1].y);
             tmem_st_wait();
             tc_fence_before();
@@ -1273,7 +1282,7 @@ __device__ __forceinline__ void many_softmax(const AttendParams& p, ManyShared<D
         const float vs = vref > kOperandLift ? __uint_as_float(static_cast<uint32_t>(vref - kOperandLift) << 23) : 0.0f;
         const float m = bound == -INFINITY ? -INFINITY : ref;
         const int64_t at = slot * kManyRows + 128 * t + tid;
-#pragma unroll
+#pragma unroll 1
         for (int b = 0; b < D / 32; ++b) {
             float2 o[16];
             tmem_ld32(to + 32 * b, *reinterpret_cast<uint32_t(*)[32]>(o));
@@ -1323,6 +1332,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) attend_many_kernel(const __gr
         }
         for (int i = 0; i < 4; ++i) mbar_init(&sm.r_full[i], 1);
         mbar_init(&sm.drained, 1);
+        for (int i = 0; i < 8; ++i) mbar_init(&sm.turn[i >> 2][i & 3], 1);
         for (int i = 0; i < kManyUnits; ++i) mbar_init(&sm.unit_full[i], 1), mbar_init(&sm.unit_free[i], 17);
         sm.abort = 0;
         fence_mbar_init();
