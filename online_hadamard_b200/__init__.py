@@ -141,7 +141,7 @@ def _check(status: int, where: str) -> None:
 
 
 def _ptr(t: torch.Tensor | None):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream(stream, device: torch.device) -> ctypes.c_void_p:
@@ -161,9 +161,18 @@ def _check_stream_device(stream, device: torch.device) -> None:
         raise ValueError(f"stream belongs to {sdev}, the call's tensors to {device}")
 
 
+_CURRENT = contextlib.nullcontext()
+
+
 def _device(device):
-    """`device` made current for the library call inside (None: the current device as it is)."""
-    return contextlib.nullcontext() if device is None else torch.cuda.device(device)
+    """`device` made current for the library call inside (None: the current device as it is).  Nothing is
+    switched where it is current already, which costs a call of a few microseconds two or three of them."""
+    if device is None:
+        return _CURRENT
+    device = torch.device(device)
+    if device.type == "cuda" and device.index in (None, torch.cuda.current_device()):
+        return _CURRENT
+    return torch.cuda.device(device)
 
 
 def _need(t: torch.Tensor, name: str, dtype: torch.dtype, shape=None, min_numel=None, device=None) -> None:
@@ -178,7 +187,7 @@ def _need(t: torch.Tensor, name: str, dtype: torch.dtype, shape=None, min_numel=
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if min_numel is not None:
         _need_numel(t, name, min_numel)
@@ -552,6 +561,14 @@ def macaq_flip_refine(W: torch.Tensor, s: torch.Tensor, Hs: torch.Tensor, Wq: to
     return moves
 
 
+def _out(t, name: str, shape, device) -> torch.Tensor:
+    """A bf16 result: the caller's tensor after its checks, or a new one."""
+    if t is None:
+        return torch.empty(shape, dtype=torch.bfloat16, device=device)
+    _need(t, name, torch.bfloat16, shape, device=device)
+    return t
+
+
 def _need_rows(t: torch.Tensor, name: str, width: int, device=None) -> int:
     """A bf16 CUDA tensor [T, >= width] whose rows are contiguous and may lie further apart (a slice of
     the columns of a stacked output); returns the distance between rows in elements."""
@@ -616,11 +633,9 @@ def macaq_qk_norm_rope(qkv: torch.Tensor, Hq: int, Hk: int, head_dim: int, rope=
     for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
         if w is not None:
             _need(w, name, torch.float32, (head_dim,), device=dev)
-    q = torch.empty(T, Hq, head_dim, dtype=torch.bfloat16, device=dev) if q is None else q
-    k = torch.empty(T, Hk, head_dim, dtype=torch.bfloat16, device=dev) if k is None else k
-    _need(q, "q", torch.bfloat16, (T, Hq, head_dim), device=dev)
-    _need(k, "k", torch.bfloat16, (T, Hk, head_dim), device=dev)
-    with torch.cuda.device(dev):
+    q = _out(q, "q", (T, Hq, head_dim), dev)
+    k = _out(k, "k", (T, Hk, head_dim), dev)
+    with _device(dev):
         _check(load_library().macaq_qk_norm_rope(_ptr(qkv), T, ld, Hq, Hk, head_dim, _ptr(q_weight), _ptr(k_weight),
                                                  eps, _ptr(rope), rows, R, 1 if interleaved else 0, _ptr(positions),
                                                  _ptr(q), _ptr(k), _stream(stream, dev)), "macaq_qk_norm_rope")
@@ -646,9 +661,8 @@ def macaq_kv4_append(qkv: torch.Tensor, Hq: int, Hk: int, head_dim: int, cache: 
         if w is not None:
             _need(w, name, torch.float32, (head_dim,), device=dev)
     if Hq:
-        q = torch.empty(T, Hq, head_dim, dtype=torch.bfloat16, device=dev) if q is None else q
-        _need(q, "q", torch.bfloat16, (T, Hq, head_dim), device=dev)
-    with torch.cuda.device(dev):
+        q = _out(q, "q", (T, Hq, head_dim), dev)
+    with _device(dev):
         _check(load_library().macaq_kv4_append(_ptr(qkv), T, ld, Hq, Hk, head_dim, _ptr(q_weight), _ptr(k_weight), eps,
                                                _ptr(rope), rows, R, 1 if interleaved else 0, _ptr(positions),
                                                _ptr(cache), pages, page_size, _ptr(slots), _ptr(q) if Hq else None,
@@ -664,11 +678,9 @@ def macaq_kv4_gather(cache: torch.Tensor, head_dim: int, page_size: int, slots: 
     dev = cache.device
     T = slots.numel()
     _need(slots, "slots", torch.int64, (T,), device=dev)
-    k = torch.empty(T, Hk, head_dim, dtype=torch.bfloat16, device=dev) if k is None else k
-    v = torch.empty(T, Hk, head_dim, dtype=torch.bfloat16, device=dev) if v is None else v
-    _need(k, "k", torch.bfloat16, (T, Hk, head_dim), device=dev)
-    _need(v, "v", torch.bfloat16, (T, Hk, head_dim), device=dev)
-    with torch.cuda.device(dev):
+    k = _out(k, "k", (T, Hk, head_dim), dev)
+    v = _out(v, "v", (T, Hk, head_dim), dev)
+    with _device(dev):
         _check(load_library().macaq_kv4_gather(_ptr(cache), pages, page_size, Hk, head_dim, _ptr(slots), T, _ptr(k),
                                                _ptr(v), _stream(stream, dev)), "macaq_kv4_gather")
     return k, v
@@ -692,9 +704,12 @@ def macaq_kv4_attention(q: torch.Tensor, cache: torch.Tensor, page_size: int, ta
     if not isinstance(q, torch.Tensor) or q.dim() != 3:
         raise ValueError("q must be a CUDA tensor of shape (T, heads, head_dim)")
     T, Hq, D = q.shape
-    if T and (q.stride(2) != 1 or (Hq > 1 and q.stride(1) != D)):
-        raise ValueError("the rows of q must be contiguous")
-    ld = _need_rows(q.as_strided((T, Hq * D), (q.stride(0), 1)), "q", Hq * D)
+    if q.is_cuda and q.dtype == torch.bfloat16 and q.is_contiguous():
+        ld = Hq * D
+    else:
+        if T and (q.stride(2) != 1 or (Hq > 1 and q.stride(1) != D)):
+            raise ValueError("the rows of q must be contiguous")
+        ld = _need_rows(q.as_strided((T, Hq * D), (q.stride(0), 1)), "q", Hq * D)
     dev = q.device
     pages, Hk = _need_cache(cache, page_size, D, dev)
     if not isinstance(tables, torch.Tensor) or tables.dim() != 2:
@@ -706,16 +721,17 @@ def macaq_kv4_attention(q: torch.Tensor, cache: torch.Tensor, page_size: int, ta
         _need(cu_q, "cu_q", torch.int32, (B + 1,), device=dev)
     elif B != T or max_q != 1:
         raise ValueError("without cu_q every sequence has one query: T = B and max_q = 1")
-    out = torch.empty(T, Hq, D, dtype=torch.bfloat16, device=dev) if out is None else out
-    _need(out, "out", torch.bfloat16, (T, Hq, D), device=dev)
+    out = _out(out, "out", (T, Hq, D), dev)
     if lse is not None:
         _need(lse, "lse", torch.float32, (T, Hq), device=dev)
     need = kv4_attention_workspace_bytes(T, B, Hq, Hk, D, max_q, dev)
     if need == 0:
         raise ValueError("shape not supported by the attention (Hq a multiple of Hk, at most 1024; max_q >= 1)")
-    workspace = torch.empty(need, dtype=torch.uint8, device=dev) if workspace is None else workspace
-    _need(workspace, "workspace", torch.uint8, min_numel=need, device=dev)
-    with torch.cuda.device(dev):
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    else:
+        _need(workspace, "workspace", torch.uint8, min_numel=need, device=dev)
+    with _device(dev):
         _check(load_library().macaq_kv4_attention(
             _ptr(q), T, ld, Hq, Hk, D, _ptr(cache), pages, page_size, _ptr(tables), B, width, _ptr(kv_lens), _ptr(cu_q),
             int(max_q), D ** -0.5 if scale is None else float(scale), int(window), _ptr(out), _ptr(lse),

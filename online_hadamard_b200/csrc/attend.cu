@@ -737,7 +737,6 @@ struct ManyShared {
     alignas(1024) uint8_t v[2][kTile];
     alignas(16) uint8_t raw[8][kRaw];
     uint64_t k_full[2], k_free[2], v_full[2], v_free[2], q_full[2], s_full[2], p_full[2], o_full[2], r_full[4], drained;
-    uint64_t turn[2][4];  // [t][w]: warp w of tile t may take its exponentials
     // of block j at [j % 4]: each K warp's largest scale and its strips (16 tokens) whose page is not there,
     // and V's reference; a slot is rewritten after the products of block j + 2, whose softmax follows that of j.  r_full: V's is there
     int k_ref[4][4], gone[4][4], v_ref[4];
@@ -1239,11 +1238,6 @@ __device__ __forceinline__ void many_softmax(const AttendParams& p, ManyShared<D
                     }
                 }
             }
-            // The exponentials of the two warps on one scheduler go in turn: together both would take twice as long, and
-            // then both wait for the products; in turn one's exponentials run beside the other's products.
-            if (t == 1 || j > 0) {
-                if (!warp_wait(&sm.turn[t][(tid >> 5) & 3], (t == 1 ? j : j - 1) & 1, &sm.abort)) return;
-            }
             float2 add[2] = {};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -1265,7 +1259,6 @@ __device__ __forceinline__ void many_softmax(const AttendParams& p, ManyShared<D
                 }
                 tmem_st16(ts + 16 * i, h);
             }
-            if ((tid & 31) == 0) mbar_arrive(&sm.turn[t ^ 1][(tid >> 5) & 3]);
             sum += (add[0].x + add[0].y) + (add[1].x + add[1].y);
             tmem_st_wait();
             tc_fence_before();
@@ -1332,7 +1325,6 @@ __global__ void __launch_bounds__(kManyThreads, 1) attend_many_kernel(const __gr
         }
         for (int i = 0; i < 4; ++i) mbar_init(&sm.r_full[i], 1);
         mbar_init(&sm.drained, 1);
-        for (int i = 0; i < 8; ++i) mbar_init(&sm.turn[i >> 2][i & 3], 1);
         for (int i = 0; i < kManyUnits; ++i) mbar_init(&sm.unit_full[i], 1), mbar_init(&sm.unit_free[i], 17);
         sm.abort = 0;
         fence_mbar_init();
@@ -1467,7 +1459,7 @@ static AttendPlan plan_attend(int64_t B, int Hq, int Hk, int D, int64_t max_q) {
     a.units = B * Hk * a.row_tiles;
     if (a.tile_rows == kManyRows) {
         a.ctas = sm_count();
-        a.unit_cost = 2;
+        a.unit_cost = 4;
     } else {  // cut while there are few units: many balance themselves, and need no joining
         const int resident = sm_count() * few_resident(a.tile_rows / 8);
         a.ctas = a.units >= 4 * resident ? 0 : resident;
@@ -1482,8 +1474,13 @@ template <int D, int NT>
 static int launch_few(const AttendParams& p, unsigned blocks, cudaStream_t stream) {
     constexpr size_t kSmem = sizeof(FewShared<D, NT>);
     static_assert(few_resident(NT) * (kSmem + 1024) <= 228 * 1024, "shared memory of an SM");
-    if (cudaFuncSetAttribute(attend_few_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess)
-        return MACAQ_ECUDA;
+    static int cache[64] = {0};
+    const int ready = cached_per_device(cache, [] {
+        return cudaFuncSetAttribute(attend_few_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) == cudaSuccess
+                   ? 1
+                   : -1;
+    });
+    if (!ready) return MACAQ_ECUDA;
     return launch_dependent_smem(attend_few_kernel<D, NT>, dim3(blocks), kFewThreads, kSmem, stream, p);
 }
 
@@ -1492,10 +1489,16 @@ static int launch_many(const AttendParams& p, cudaStream_t stream) {
     constexpr size_t kSmem = sizeof(ManyShared<D>) + 1024;
     static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
     // setmaxnreg.inc takes registers from those the CTA was launched with: with fewer it would wait forever
-    cudaFuncAttributes fa;
-    if (cudaFuncGetAttributes(&fa, attend_many_kernel<D>) != cudaSuccess || fa.numRegs < kManyLaunchRegs) return MACAQ_ECUDA;
-    if (cudaFuncSetAttribute(attend_many_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess)
-        return MACAQ_ECUDA;
+    static int cache[64] = {0};
+    const int ready = cached_per_device(cache, [] {
+        cudaFuncAttributes fa;
+        return cudaFuncGetAttributes(&fa, attend_many_kernel<D>) == cudaSuccess && fa.numRegs >= kManyLaunchRegs &&
+                       cudaFuncSetAttribute(attend_many_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) ==
+                           cudaSuccess
+                   ? 1
+                   : -1;
+    });
+    if (!ready) return MACAQ_ECUDA;
     return launch_dependent_smem(attend_many_kernel<D>, dim3(p.ctas), kManyThreads, kSmem, stream, p);
 }
 
