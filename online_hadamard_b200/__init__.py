@@ -144,14 +144,13 @@ def _ptr(t: torch.Tensor | None):
     return None if t is None else t.data_ptr()
 
 
-def _stream(stream, device: torch.device) -> ctypes.c_void_p:
+def _stream(stream, device: torch.device) -> int:
     """The CUDA stream handle of a call whose tensors live on `device`: the given stream, which
     must belong to that device, or that device's current stream."""
     if stream is None:
-        stream = torch.cuda.current_stream(device)
-    else:
-        _check_stream_device(stream, device)
-    return ctypes.c_void_p(stream.cuda_stream)
+        return torch._C._cuda_getCurrentRawStream(device.index)  # without a Stream object around it
+    _check_stream_device(stream, device)
+    return stream.cuda_stream
 
 
 def _check_stream_device(stream, device: torch.device) -> None:
@@ -169,8 +168,7 @@ def _device(device):
     switched where it is current already, which costs a call of a few microseconds two or three of them."""
     if device is None:
         return _CURRENT
-    device = torch.device(device)
-    if device.type == "cuda" and device.index in (None, torch.cuda.current_device()):
+    if isinstance(device, torch.device) and device.index == torch.cuda.current_device() and device.type == "cuda":
         return _CURRENT
     return torch.cuda.device(device)
 
@@ -561,11 +559,11 @@ def macaq_flip_refine(W: torch.Tensor, s: torch.Tensor, Hs: torch.Tensor, Wq: to
     return moves
 
 
-def _out(t, name: str, shape, device) -> torch.Tensor:
-    """A bf16 result: the caller's tensor after its checks, or a new one."""
+def _out(t, name: str, shape, like: torch.Tensor) -> torch.Tensor:
+    """A bf16 result on the device of `like`: the caller's tensor after its checks, or a new one."""
     if t is None:
-        return torch.empty(shape, dtype=torch.bfloat16, device=device)
-    _need(t, name, torch.bfloat16, shape, device=device)
+        return like.new_empty(shape, dtype=torch.bfloat16)
+    _need(t, name, torch.bfloat16, shape, device=like.device)
     return t
 
 
@@ -633,8 +631,8 @@ def macaq_qk_norm_rope(qkv: torch.Tensor, Hq: int, Hk: int, head_dim: int, rope=
     for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
         if w is not None:
             _need(w, name, torch.float32, (head_dim,), device=dev)
-    q = _out(q, "q", (T, Hq, head_dim), dev)
-    k = _out(k, "k", (T, Hk, head_dim), dev)
+    q = _out(q, "q", (T, Hq, head_dim), qkv)
+    k = _out(k, "k", (T, Hk, head_dim), qkv)
     with _device(dev):
         _check(load_library().macaq_qk_norm_rope(_ptr(qkv), T, ld, Hq, Hk, head_dim, _ptr(q_weight), _ptr(k_weight),
                                                  eps, _ptr(rope), rows, R, 1 if interleaved else 0, _ptr(positions),
@@ -661,7 +659,7 @@ def macaq_kv4_append(qkv: torch.Tensor, Hq: int, Hk: int, head_dim: int, cache: 
         if w is not None:
             _need(w, name, torch.float32, (head_dim,), device=dev)
     if Hq:
-        q = _out(q, "q", (T, Hq, head_dim), dev)
+        q = _out(q, "q", (T, Hq, head_dim), qkv)
     with _device(dev):
         _check(load_library().macaq_kv4_append(_ptr(qkv), T, ld, Hq, Hk, head_dim, _ptr(q_weight), _ptr(k_weight), eps,
                                                _ptr(rope), rows, R, 1 if interleaved else 0, _ptr(positions),
@@ -678,8 +676,8 @@ def macaq_kv4_gather(cache: torch.Tensor, head_dim: int, page_size: int, slots: 
     dev = cache.device
     T = slots.numel()
     _need(slots, "slots", torch.int64, (T,), device=dev)
-    k = _out(k, "k", (T, Hk, head_dim), dev)
-    v = _out(v, "v", (T, Hk, head_dim), dev)
+    k = _out(k, "k", (T, Hk, head_dim), cache)
+    v = _out(v, "v", (T, Hk, head_dim), cache)
     with _device(dev):
         _check(load_library().macaq_kv4_gather(_ptr(cache), pages, page_size, Hk, head_dim, _ptr(slots), T, _ptr(k),
                                                _ptr(v), _stream(stream, dev)), "macaq_kv4_gather")
@@ -721,7 +719,7 @@ def macaq_kv4_attention(q: torch.Tensor, cache: torch.Tensor, page_size: int, ta
         _need(cu_q, "cu_q", torch.int32, (B + 1,), device=dev)
     elif B != T or max_q != 1:
         raise ValueError("without cu_q every sequence has one query: T = B and max_q = 1")
-    out = _out(out, "out", (T, Hq, D), dev)
+    out = _out(out, "out", (T, Hq, D), q)
     if lse is not None:
         _need(lse, "lse", torch.float32, (T, Hq), device=dev)
     need = kv4_attention_workspace_bytes(T, B, Hq, Hk, D, max_q, dev)
