@@ -24,6 +24,13 @@ namespace macaq {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
+// The unit that a CTA's range ends in, if the range holds its beginning but not its end: `parts` CTAs, this one
+// and the next, hold it (0: there is none).
+struct __align__(16) CutUnit {
+    int64_t row0;  // its sequence's first query row
+    int r0, nrows, kvh, parts, unused[2];
+};
+
 struct AttendParams {
     const uint16_t* q;  // bf16 [T][ldq]
     int64_t T, ldq;
@@ -46,6 +53,7 @@ struct AttendParams {
     int tile_rows, row_tiles, ctas, unit_cost;
     float* part_o;    // fp32 [ctas][2][tile_rows][D], each row divided by its own sum
     float2* part_ml;  // [ctas][2][tile_rows]: its reference m (base 2) and sum of 2^(s - m)
+    CutUnit* cuts;    // [ctas]
 };
 
 // Sequence b: its first query row, its queries, its keys and its first query's position (negative
@@ -173,11 +181,11 @@ struct Unit {
     int64_t slot;
 };
 struct Walk {
-    int64_t pos, end, item, item_pos;
-    Walk() = default;
+    int64_t pos, end, item, item_pos, len;
+    CutUnit cut = {};
     __device__ __forceinline__ Walk(const AttendParams& p, const Place& c)
-        : pos(c.pos), end(c.pos + c.len < c.total ? c.pos + c.len : c.total), item(c.item), item_pos(c.item_pos) {}
-    __device__ __forceinline__ Walk(uint32_t unit, uint32_t Hk) : pos(unit % Hk), end(-1), item(unit / Hk), item_pos(0) {}
+        : pos(c.pos), end(c.pos + c.len < c.total ? c.pos + c.len : c.total), item(c.item), item_pos(c.item_pos), len(c.len) {}
+    __device__ __forceinline__ Walk(uint32_t unit, uint32_t Hk) : pos(unit % Hk), end(-1), item(unit / Hk), item_pos(0), len(1) {}
     __device__ __forceinline__ bool next(const AttendParams& p, int shift, Unit& u) {
         if (!p.ctas) {  // one unit
             if (end == 0) return false;
@@ -204,6 +212,8 @@ struct Walk {
             if (to <= from) continue;
             u.begin = (u.t.sp.first_lo >> shift) + from, u.end = u.begin + to - from;
             u.slot = from == 0 && to == u.t.blocks ? -1 : 2 * static_cast<int64_t>(blockIdx.x) + (from == 0 ? 1 : 0);
+            if (from == 0 && to < u.t.blocks)  // (a range is much shorter than 2^31 blocks where it cuts anything)
+                cut = {u.t.s.row0, u.t.r0, u.t.nrows, u.kvh, 1 + static_cast<int>((u.t.blocks - to + len - 1) / len), {0, 0}};
             return true;
         }
         return false;
@@ -701,6 +711,7 @@ __global__ void __launch_bounds__(kFewThreads, few_resident(NT)) attend_few_kern
     Walk walk = p.ctas ? Walk(p, place) : Walk(blockIdx.x, p.Hk);
     Unit unit;
     while (walk.next(p, kFewShift, unit)) few_unit<D, NT>(p, sm, unit);
+    if (p.ctas && threadIdx.x == 0) p.cuts[blockIdx.x] = walk.cut;
 }
 
 // ------------------------------------------------------------------------------ many query rows
@@ -782,6 +793,7 @@ __device__ __forceinline__ void many_units(const AttendParams& p, ManyShared<D>&
             mbar_arrive(&sm.unit_full[at]);
         }
     }
+    if (lane == 0) p.cuts[blockIdx.x] = walk.cut;
 }
 
 __device__ __forceinline__ void group_sync(int id) { asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory"); }
@@ -1368,76 +1380,97 @@ __global__ void __launch_bounds__(kManyThreads, 1) attend_many_kernel(const __gr
     if (warp == 16) tmem_dealloc(sm.tmem, 512);
 }
 
-// Joins the parts of the units that were cut: CTA (i, y) looks at the boundary of ranges i and i + 1, and if it is
-// the first one inside a unit, joins that unit's rows y, y + gridDim.y, .. (a warp a row).
-template <int D>
-__global__ void __launch_bounds__(128) attend_join_kernel(const __grid_constant__ AttendParams p, int shift) {
-    constexpr int kElems = D / 32;  // of a lane, neighbours
-    __shared__ PlaceShared place;
+// Joins the parts of the units that were cut: CTA (i, y) those of the unit that range i ends in.  SPREAD: row y, its
+// parts spread over the warps (few rows of many parts); otherwise a warp a row (many rows of two or three).
+template <int D, bool SPREAD>
+__global__ void __launch_bounds__(128) attend_join_kernel(const __grid_constant__ AttendParams p) {
+    constexpr int kElems = D / 32, kWarps = SPREAD ? 4 : 1;  // elements of a lane, neighbours; warps of a row
+    __shared__ float o_s[kWarps][D];
+    __shared__ float2 ml_s[kWarps];
     griddep_launch_dependents();
     griddep_wait();
-    const int lane = threadIdx.x & 31;
-    const Place c = find_place<128>(p, shift, blockIdx.x + 1, place);
-    if (c.pos >= c.total) return;
-    const Tile t = tile_of(p, c.item, shift);
-    const int per = t.blocks + p.unit_cost;
-    const int kvh = static_cast<int>((c.pos - c.item_pos) / per);
-    const int64_t u0 = c.item_pos + static_cast<int64_t>(kvh) * per + p.unit_cost;  // the unit's first block
-    const int64_t c0 = blockIdx.x;  // the CTA that holds it, if it is a unit to join
-    if (u0 >= c.pos || u0 < c.pos - c.len) return;
-    const int parts = static_cast<int>((u0 + t.blocks - 1) / c.len - c0) + 1;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const CutUnit u = p.cuts[blockIdx.x];
+    const int r = SPREAD ? blockIdx.y : blockIdx.y * 4 + warp;
+    if (u.parts == 0 || r >= u.nrows) return;
     // the first part is what its CTA's range ends in (slot 1), the others are what theirs begin with (slot 0)
-    const int64_t stride = 2 * p.tile_rows;
-    for (int r = blockIdx.y * 4 + (threadIdx.x >> 5); r < t.nrows; r += 4 * gridDim.y) {
-        const int64_t at = c0 * stride + r;
-        auto place_of = [&](int k) { return at + k * stride + (k == 0 ? p.tile_rows : 0); };
-        float m = -INFINITY;
-        for (int k = lane; k < parts; k += 32) m = fmaxf(m, p.part_ml[place_of(k)].x);
+    const int64_t at = static_cast<int64_t>(blockIdx.x) * 2 * p.tile_rows + r;
+    auto place_of = [&](int k) { return at + static_cast<int64_t>(k) * 2 * p.tile_rows + (k == 0 ? p.tile_rows : 0); };
+    const int k0 = SPREAD ? warp : 0;
+    float m = -INFINITY, total = 0.0f, o[kElems] = {};
+    for (int base = k0; base < u.parts; base += 32 * kWarps) {  // up to 32 parts at a time, one a lane
+        const int mine = base + kWarps * lane;
+        float2 ml = make_float2(-INFINITY, 0.0f);
+        if (mine < u.parts) ml = p.part_ml[place_of(mine)];
+        float top = ml.x;
 #pragma unroll
-        for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, x));
-        float total = 0.0f, o[kElems] = {};
-        for (int k0 = 0; k0 < parts; k0 += 32) {
-            float w = 0.0f;  // of part k0 + lane
-            if (k0 + lane < parts) {
-                const float2 ml = p.part_ml[place_of(k0 + lane)];
-                if (ml.x != -INFINITY) w = exp2_approx(ml.x - m) * ml.y;
-            }
-            const int n = min(32, parts - k0);
-#pragma unroll 4
-            for (int k = 0; k < n; ++k) {
-                const float wk = __shfl_sync(0xFFFFFFFFu, w, k);
-                const float* src = p.part_o + place_of(k0 + k) * D + kElems * lane;
-                total += wk;
+        for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, x));
+        if (top > m) {
+            const float shift = m == -INFINITY ? 0.0f : exp2_approx(m - top);
+            total *= shift;
 #pragma unroll
-                for (int j = 0; j < kElems; ++j) o[j] += wk == 0.0f ? 0.0f : wk * src[j];
-            }
+            for (int j = 0; j < kElems; ++j) o[j] *= shift;
+            m = top;
         }
-        const float inv = total > 0.0f ? kHadamardNorm / total : total == 0.0f ? 0.0f : total;
+        const float w = ml.x == -INFINITY ? 0.0f : exp2_approx(ml.x - m) * ml.y;
+        const int n = min(32, (u.parts - base + kWarps - 1) / kWarps);
+#pragma unroll 8
+        for (int k = 0; k < n; ++k) {
+            const float wk = __shfl_sync(0xFFFFFFFFu, w, k);
+            const float* src = p.part_o + place_of(base + kWarps * k) * D + kElems * lane;
+            float x[kElems];
+            if constexpr (kElems == 4)
+                *reinterpret_cast<float4*>(x) = *reinterpret_cast<const float4*>(src);
+            else
+                *reinterpret_cast<float2*>(x) = *reinterpret_cast<const float2*>(src);
+            total += wk;
 #pragma unroll
-        for (int j = 0; j < kElems; ++j) o[j] *= inv;
-#pragma unroll
-        for (int x = 1; x < kElems; x <<= 1)  // distances inside the lane
-#pragma unroll
-            for (int j = 0; j < kElems; ++j)
-                if ((j & x) == 0) {
-                    const float a = o[j], z = o[j + x];
-                    o[j] = a + z, o[j + x] = a - z;
-                }
-#pragma unroll
-        for (int x = 1; x * kElems < 32; x <<= 1) {
-#pragma unroll
-            for (int j = 0; j < kElems; ++j) {
-                const float y = __shfl_xor_sync(0xFFFFFFFFu, o[j], x);
-                o[j] = lane & x ? y - o[j] : o[j] + y;
-            }
+            for (int j = 0; j < kElems; ++j) o[j] += wk == 0.0f ? 0.0f : wk * x[j];
         }
-        const int qi = (t.r0 + r) / p.G;
-        const int64_t row = (t.s.row0 + qi) * p.Hq + kvh * p.G + (t.r0 + r) - qi * p.G;
-        uint16_t* dst = p.out + row * D + kElems * lane;
-#pragma unroll
-        for (int j = 0; j < kElems; j += 2) *reinterpret_cast<uint32_t*>(dst + j) = pack_bf16(o[j], o[j + 1]);
-        if (p.lse && lane == 0) p.lse[row] = total == 0.0f ? -INFINITY : (m + log2f(total)) * kLn2;
     }
+    if constexpr (SPREAD) {
+        if (lane == 0) ml_s[warp] = make_float2(m, total);
+#pragma unroll
+        for (int j = 0; j < kElems; ++j) o_s[warp][kElems * lane + j] = o[j];
+        __syncthreads();
+        if (warp) return;
+        m = fmaxf(fmaxf(ml_s[0].x, ml_s[1].x), fmaxf(ml_s[2].x, ml_s[3].x));
+        total = 0.0f;
+#pragma unroll
+        for (int j = 0; j < kElems; ++j) o[j] = 0.0f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float w = ml_s[k].x == -INFINITY ? 0.0f : exp2_approx(ml_s[k].x - m);
+            total += w * ml_s[k].y;
+#pragma unroll
+            for (int j = 0; j < kElems; ++j) o[j] += w == 0.0f ? 0.0f : w * o_s[k][kElems * lane + j];
+        }
+    }
+    const float inv = total > 0.0f ? kHadamardNorm / total : total == 0.0f ? 0.0f : total;
+#pragma unroll
+    for (int j = 0; j < kElems; ++j) o[j] *= inv;
+#pragma unroll
+    for (int x = 1; x < kElems; x <<= 1)  // distances inside the lane
+#pragma unroll
+        for (int j = 0; j < kElems; ++j)
+            if ((j & x) == 0) {
+                const float a = o[j], z = o[j + x];
+                o[j] = a + z, o[j + x] = a - z;
+            }
+#pragma unroll
+    for (int x = 1; x * kElems < 32; x <<= 1) {
+#pragma unroll
+        for (int j = 0; j < kElems; ++j) {
+            const float y = __shfl_xor_sync(0xFFFFFFFFu, o[j], x);
+            o[j] = lane & x ? y - o[j] : o[j] + y;
+        }
+    }
+    const int qi = (u.r0 + r) / p.G;
+    const int64_t row = (u.row0 + qi) * p.Hq + u.kvh * p.G + (u.r0 + r) - qi * p.G;
+    uint16_t* dst = p.out + row * D + kElems * lane;
+#pragma unroll
+    for (int j = 0; j < kElems; j += 2) *reinterpret_cast<uint32_t*>(dst + j) = pack_bf16(o[j], o[j + 1]);
+    if (p.lse && lane == 0) p.lse[row] = total == 0.0f ? -INFINITY : (m + log2f(total)) * kLn2;
 }
 
 // ------------------------------------------------------------------------------------ host side
@@ -1463,9 +1496,9 @@ static AttendPlan plan_attend(int64_t B, int Hq, int Hk, int D, int64_t max_q) {
     } else {  // cut while there are few units: many balance themselves, and need no joining
         const int resident = sm_count() * few_resident(a.tile_rows / 8);
         a.ctas = a.units >= 4 * resident ? 0 : resident;
-        a.unit_cost = 8;
+        a.unit_cost = 16;
     }
-    a.bytes = static_cast<size_t>(a.ctas) * 2 * a.tile_rows * (static_cast<size_t>(D) * 4 + 8);
+    a.bytes = static_cast<size_t>(a.ctas) * (2 * a.tile_rows * (static_cast<size_t>(D) * 4 + 8) + sizeof(CutUnit));
     a.bytes = (a.bytes + 255) / 256 * 256 + 256;
     return a;
 }
@@ -1512,8 +1545,9 @@ static int launch_attend(const AttendParams& p, int64_t units, cudaStream_t stre
                    : p.tile_rows == 16 ? launch_few<D, 2>(p, n, stream)
                                        : launch_few<D, 4>(p, n, stream);
     if (st != MACAQ_OK || p.ctas < 2) return st;
-    return launch_dependent(attend_join_kernel<D>, dim3(p.ctas - 1, p.tile_rows / 8), 128, stream, p,
-                            p.tile_rows == kManyRows ? kManyShift : kFewShift);
+    if (p.tile_rows == kManyRows)
+        return launch_dependent(attend_join_kernel<D, false>, dim3(p.ctas - 1, kManyRows / 4), 128, stream, p);
+    return launch_dependent(attend_join_kernel<D, true>, dim3(p.ctas - 1, p.tile_rows), 128, stream, p);
 }
 
 }  // namespace macaq
@@ -1553,7 +1587,8 @@ extern "C" int macaq_kv4_attention(const uint16_t* q, int64_t T, int64_t ldq, in
     p.scale_log2 = scale * kLog2e, p.window = static_cast<int>(window < kMaxDim ? window : 0), p.out = out, p.lse = lse;
     p.tile_rows = plan.tile_rows, p.row_tiles = plan.row_tiles, p.ctas = plan.ctas;
     p.unit_cost = plan.unit_cost;
-    p.part_ml = static_cast<float2*>(workspace);
+    p.cuts = static_cast<CutUnit*>(workspace);
+    p.part_ml = reinterpret_cast<float2*>(p.cuts + p.ctas);
     p.part_o = reinterpret_cast<float*>(p.part_ml + static_cast<int64_t>(p.ctas) * 2 * p.tile_rows);
     const auto s = static_cast<cudaStream_t>(stream);
     return head_dim == 64 ? launch_attend<64>(p, plan.units, s) : launch_attend<128>(p, plan.units, s);
