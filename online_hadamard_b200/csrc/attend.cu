@@ -761,11 +761,19 @@ struct ManyShared {
     uint64_t unit_full[kManyUnits], unit_free[kManyUnits];
 };
 
-// mbar_wait with one answer for the whole warp.
+// Waits for the phase with the given parity, with one answer for the whole warp: false (and the abort flag and
+// the device status are set) after some 4 s, which means a logic error.  A few instructions, since every
+// role has several of these in its loop, and the roles' loops share one instruction cache.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int* abort) {
-    if (__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity))) return true;
-    const bool ok = mbar_wait(bar, parity, abort);
-    return __all_sync(0xFFFFFFFFu, ok);
+    constexpr uint32_t kPause = 2000;  // ns
+    for (int n = 0; !__all_sync(0xFFFFFFFFu, mbar_try_wait_for(bar, parity, kPause)); ++n) {
+        if (__any_sync(0xFFFFFFFFu, *reinterpret_cast<volatile int*>(abort) != 0) || n > 2000000) {
+            atomicExch(&g_device_status, MACAQ_ETIMEOUT);
+            *reinterpret_cast<volatile int*>(abort) = 1;
+            return false;
+        }
+    }
+    return true;
 }
 
 // A warp's next unit: waits for number n, and gives number n - 1 back first.  False: there is none.
@@ -1069,7 +1077,7 @@ __device__ __forceinline__ void many_products(ManyShared<D>& sm, int lane) {
         const int n = unit.end - unit.begin;
         for (int i = 0; i < n; ++i, ++j) {
             if (!warp_wait(&sm.k_full[j & 1], (j >> 1) & 1, &sm.abort)) return;
-#pragma unroll
+#pragma unroll 1
             for (int t = 0; t < 2; ++t) {
                 if (i == 0) {
                     if (!warp_wait(&sm.q_full[t], units & 1, &sm.abort)) return;
@@ -1092,7 +1100,7 @@ __device__ __forceinline__ void many_products(ManyShared<D>& sm, int lane) {
                 __syncwarp();
             }
         }
-#pragma unroll
+#pragma unroll 1
         for (int t = 0; t < 2; ++t) {
             if (!values(t, j - 1, n == 1)) return;
             if (elect_one()) {
@@ -1169,13 +1177,61 @@ __device__ __forceinline__ void many_softmax(const AttendParams& p, ManyShared<D
     const uint32_t lanes = static_cast<uint32_t>(tid & 96) << 16;  // the warp's 32 lanes of tensor memory
     const uint32_t ts = sm.tmem + 128 * t + lanes, to = sm.tmem + 256 + 128 * t + lanes;
     int j = 0, units = 0;
-    bool more = next_unit<D>(sm, 0, tid & 31);
-    if (!more) return;
-    QueryRow row = load_query<D>(p, sm, sm.unit[0], t, tid);
-    while (more) {
+    float ref = 0.0f, bound = -INFINITY, sum = 0.0f;
+    int vref = 0;
+    int64_t slot = -1;
+    QueryRow row = {0, -1, -1, 1.0f};
+    for (;; ++units) {
+        // this unit's queries (the last one's have been used: its last scores are there), then the last one's results
+        const int64_t out = row.out, out_slot = slot;
+        const bool more = next_unit<D>(sm, units, tid & 31);
         const Unit& unit = sm.unit[units % kManyUnits];
-        float ref = 0.0f, bound = -INFINITY, sum = 0.0f;
-        int vref = 0;
+        if (more) {
+            row = load_query<D>(p, sm, unit, t, tid);
+            slot = unit.slot;
+        }
+        if (units > 0) {
+            if (!warp_wait(&sm.o_full[t], (units - 1) & 1, &sm.abort)) return;
+            tc_fence_after();
+            const float inv = sum > 0.0f ? 1.0f / sum : sum == 0.0f ? 0.0f : sum;
+            const float vs = vref > kOperandLift ? __uint_as_float(static_cast<uint32_t>(vref - kOperandLift) << 23) : 0.0f;
+            const float m = bound == -INFINITY ? -INFINITY : ref;
+            const int64_t at = out_slot * kManyRows + 128 * t + tid;
+#pragma unroll 1
+            for (int b = 0; b < D / 32; ++b) {
+                float2 o[16];
+                tmem_ld32(to + 32 * b, *reinterpret_cast<uint32_t(*)[32]>(o));
+                tmem_ld_wait();
+                const float2 i2 = make_float2(inv, inv), v2 = make_float2(vs, vs);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) o[i] = __fmul2_rn(__fmul2_rn(o[i], i2), v2);
+                if (out < 0) continue;
+                if (out_slot >= 0) {
+                    float4* dst = reinterpret_cast<float4*>(p.part_o + at * D + 32 * b);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) dst[i] = make_float4(o[2 * i].x, o[2 * i].y, o[2 * i + 1].x, o[2 * i + 1].y);
+                } else {
+                    float2 n[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) n[i] = make_float2(kHadamardNorm, kHadamardNorm);
+                    scale_fwht32(o, n);
+                    uint4* dst = reinterpret_cast<uint4*>(p.out + out * D + 32 * b);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        dst[i] = make_uint4(pack_bf16(o[4 * i].x, o[4 * i].y), pack_bf16(o[4 * i + 1].x, o[4 * i + 1].y),
+                                            pack_bf16(o[4 * i + 2].x, o[4 * i + 2].y), pack_bf16(o[4 * i + 3].x, o[4 * i + 3].y));
+                }
+            }
+            tc_fence_before();
+            if (out >= 0) {
+                if (out_slot >= 0)
+                    p.part_ml[at] = make_float2(m, sum);
+                else if (p.lse)
+                    p.lse[out] = sum == 0.0f ? -INFINITY : (m + log2f(sum)) * kLn2;
+            }
+        }
+        if (!more) return;
+        ref = 0.0f, bound = -INFINITY, sum = 0.0f, vref = 0;
         const int begin = unit.begin, end = unit.end;
         for (int block = begin; block < end; ++block, ++j) {
             if (!warp_wait(&sm.r_full[j & 3], (j >> 2) & 1, &sm.abort)) return;
@@ -1275,49 +1331,6 @@ __device__ __forceinline__ void many_softmax(const AttendParams& p, ManyShared<D
             tmem_st_wait();
             tc_fence_before();
             mbar_arrive(&sm.p_full[t]);
-        }
-        // the next unit's queries (this one's have been used: its last scores are there), then this one's results
-        const int64_t out = row.out, slot = unit.slot;
-        more = next_unit<D>(sm, units + 1, tid & 31);
-        if (more) row = load_query<D>(p, sm, sm.unit[(units + 1) % kManyUnits], t, tid);
-        if (!warp_wait(&sm.o_full[t], units & 1, &sm.abort)) return;
-        ++units;
-        tc_fence_after();
-        const float inv = sum > 0.0f ? 1.0f / sum : sum == 0.0f ? 0.0f : sum;
-        const float vs = vref > kOperandLift ? __uint_as_float(static_cast<uint32_t>(vref - kOperandLift) << 23) : 0.0f;
-        const float m = bound == -INFINITY ? -INFINITY : ref;
-        const int64_t at = slot * kManyRows + 128 * t + tid;
-#pragma unroll 1
-        for (int b = 0; b < D / 32; ++b) {
-            float2 o[16];
-            tmem_ld32(to + 32 * b, *reinterpret_cast<uint32_t(*)[32]>(o));
-            tmem_ld_wait();
-            const float2 i2 = make_float2(inv, inv), v2 = make_float2(vs, vs);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) o[i] = __fmul2_rn(__fmul2_rn(o[i], i2), v2);
-            if (out < 0) continue;
-            if (slot >= 0) {
-                float4* dst = reinterpret_cast<float4*>(p.part_o + at * D + 32 * b);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) dst[i] = make_float4(o[2 * i].x, o[2 * i].y, o[2 * i + 1].x, o[2 * i + 1].y);
-            } else {
-                float2 n[16];
-#pragma unroll
-                for (int i = 0; i < 16; ++i) n[i] = make_float2(kHadamardNorm, kHadamardNorm);
-                scale_fwht32(o, n);
-                uint4* dst = reinterpret_cast<uint4*>(p.out + out * D + 32 * b);
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    dst[i] = make_uint4(pack_bf16(o[4 * i].x, o[4 * i].y), pack_bf16(o[4 * i + 1].x, o[4 * i + 1].y),
-                                        pack_bf16(o[4 * i + 2].x, o[4 * i + 2].y), pack_bf16(o[4 * i + 3].x, o[4 * i + 3].y));
-            }
-        }
-        tc_fence_before();
-        if (out >= 0) {
-            if (slot >= 0)
-                p.part_ml[at] = make_float2(m, sum);
-            else if (p.lse)
-                p.lse[out] = sum == 0.0f ? -INFINITY : (m + log2f(sum)) * kLn2;
         }
     }
 }
