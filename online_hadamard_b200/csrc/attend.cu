@@ -724,17 +724,18 @@ __global__ void __launch_bounds__(kFewThreads, few_resident(NT)) attend_few_kern
 //   warpgroup 2      K: codes to f16 in shared memory, K-major
 //   warpgroup 3      V: likewise, elements along the rows (MN-major, as V's codes lie)
 //   warp 17          finds the CTA's units
-//   warp 16          issues S_t = Q_t K^T and O_t += P_t V (tcgen05, f16 operands, fp32 sums)
-// so the two tiles' matrix products and exponentials alternate, and the codes of the next blocks are widened
-// meanwhile.  In tensor memory stand S_0, S_1 (each 128 columns, its first 64 then P) and O_0, O_1.
+//   warps 16, 18     issue S_t = Q_t K^T and O_t += P_t V of one tile each (tcgen05, f16 operands, fp32 sums)
+// so matrix products, exponentials and the widening of the next blocks' codes run side by side.  A block is worked on
+// in halves of 64 keys: in tensor memory stand S_0, S_1 (two halves of 64 columns each, the first 32 of a half
+// then P) and O_0, O_1 (128 each), so that a half's scores are there before the softmax of the one ahead ends.
 // E2M1 times a power of two is exact in f16: K is held relative to the largest scale of a warp's 32 tokens (which
 // goes into those columns' score factor), V relative to a reference above the largest scale met (rescaled like
 // the softmax reference when it moves), with 2^12 on top, so scales down to 2^-26 of the largest are exact.
 constexpr int kManyShift = 7;
 constexpr int kManyRows = 256;
 constexpr int kManyThreads = 640;
-// Registers of a thread: 96 at launch (640 threads), then split 144 / 72 / 48 (softmax / codes / products).
-constexpr int kManyLaunchRegs = 96, kSoftmaxRegs = 144, kCodeRegs = 72, kIssueRegs = 48;
+// Registers of a thread: 96 at launch (640 threads), then split 112 / 96 / 64 (softmax / codes / products).
+constexpr int kManyLaunchRegs = 96, kSoftmaxRegs = 112, kCodeRegs = 96, kIssueRegs = 64;
 static_assert(2 * kSoftmaxRegs + 2 * kCodeRegs + kIssueRegs <= 5 * kManyLaunchRegs, "registers of a CTA");
 constexpr int kOperandLift = 12;
 constexpr int kManyUnits = 4;
@@ -747,7 +748,8 @@ struct ManyShared {
     alignas(1024) uint8_t k[2][kTile];
     alignas(1024) uint8_t v[2][kTile];
     alignas(16) uint8_t raw[8][kRaw];
-    uint64_t k_full[2], k_free[2], v_full[2], v_free[2], q_full[2], s_full[2], p_full[2], o_full[2], r_full[4], drained;
+    uint64_t k_full[2], k_free[2], v_full[2], v_free[2], q_full[2], s_full[2][2], p_full[2][2], o_done[2], o_full[2];
+    uint64_t r_full[4], drained[2];
     // of block j at [j % 4]: each K warp's largest scale and its strips (16 tokens) whose page is not there,
     // and V's reference; a slot is rewritten after the products of block j + 2, whose softmax follows that of j.  r_full: V's is there
     int k_ref[4][4], gone[4][4], v_ref[4];
@@ -756,7 +758,7 @@ struct ManyShared {
     uint32_t tmem;
     PlaceShared place;
     // the CTA's units in order, written by one warp (so that no other spends registers on finding them) and read
-    // by the 17 that work on them; past the last one stands an empty one
+    // by the 18 that work on them; past the last one stands an empty one
     Unit unit[kManyUnits];
     uint64_t unit_full[kManyUnits], unit_free[kManyUnits];
 };
@@ -1046,70 +1048,58 @@ __device__ __forceinline__ void many_values(const AttendParams& p, ManyShared<D>
     cp_async_wait<0>();
 }
 
-// One warp: the matrix products of all units, issued by one of its lanes.
+// One warp: the matrix products of tile t, issued by one of its lanes.
 template <int D>
-__device__ __forceinline__ void many_products(ManyShared<D>& sm, int lane) {
+__device__ __forceinline__ void many_products(ManyShared<D>& sm, int t, int lane) {
     constexpr uint32_t kF32 = 1u << 4;  // fp32 sums, f16 operands
-    constexpr uint32_t kScoreDesc = kF32 | ((128u >> 3) << 17) | ((128u >> 4) << 24);
+    constexpr uint32_t kScoreDesc = kF32 | ((64u >> 3) << 17) | ((128u >> 4) << 24);
     constexpr uint32_t kValueDesc = kF32 | (1u << 16) | (static_cast<uint32_t>(D >> 3) << 17) | ((128u >> 4) << 24);
-    const uint32_t tm = sm.tmem;
-    const uint64_t q0 = desc_sw128(smem_u32(sm.q[0])), k0 = desc_sw128(smem_u32(sm.k[0]));
+    constexpr uint32_t kNext = ManyShared<D>::kTile >> 4, kHalf = 64 * 128 >> 4;
+    const uint32_t tm = sm.tmem + 128 * t;
+    const uint64_t qd = desc_sw128(smem_u32(sm.q[t])), k0 = desc_sw128(smem_u32(sm.k[0]));
     const uint64_t v0 = desc_mn_sw128(smem_u32(sm.v[0]), 16384);
-    constexpr uint32_t kNext = ManyShared<D>::kTile >> 4;
     int j = 0, units = 0;
-    // O_t (+)= P_t V of block i
-    auto values = [&](int t, int i, bool first) -> bool {
-        if (!warp_wait(&sm.p_full[t], i & 1, &sm.abort)) return false;
-        if (t == 0 && !warp_wait(&sm.v_full[i & 1], (i >> 1) & 1, &sm.abort)) return false;
-        tc_fence_after();
-        const uint64_t vd = v0 + (i & 1) * kNext;
-        if (elect_one()) {
-#pragma unroll 2
-            for (int k = 0; k < 8; ++k)
-                tc_mma_f16_ts(tm + 256 + 128 * t, tm + 128 * t + 8 * k, vd + (k * 2048 >> 4), kValueDesc,
-                              first && k == 0 ? 0u : 1u);
-        }
-        __syncwarp();
-        return true;
-    };
-    while (next_unit<D>(sm, units, lane)) {
+    for (; next_unit<D>(sm, units, lane); ++units) {
         const Unit& unit = sm.unit[units % kManyUnits];
-        const int n = unit.end - unit.begin;
-        for (int i = 0; i < n; ++i, ++j) {
-            if (!warp_wait(&sm.k_full[j & 1], (j >> 1) & 1, &sm.abort)) return;
+        const int halves = 2 * (unit.end - unit.begin);
+        if (!warp_wait(&sm.q_full[t], units & 1, &sm.abort)) return;
 #pragma unroll 1
-            for (int t = 0; t < 2; ++t) {
-                if (i == 0) {
-                    if (!warp_wait(&sm.q_full[t], units & 1, &sm.abort)) return;
-                } else if (!values(t, j - 1, i == 1)) {
-                    return;
-                }
+        for (int h = 0; h <= halves; ++h) {
+            if (h < halves) {  // S = Q K^T of half h
+                const int b = j + (h >> 1), half = h & 1;
+                if (half == 0 && !warp_wait(&sm.k_full[b & 1], (b >> 1) & 1, &sm.abort)) return;
                 tc_fence_after();
-                const uint64_t qd = q0 + t * kNext, kd = k0 + (j & 1) * kNext;
+                const uint64_t kd = k0 + (b & 1) * kNext + half * kHalf;
                 if (elect_one()) {
-                    if (t == 1 && i != 0) tc_commit(&sm.v_free[(j - 1) & 1]);
-#pragma unroll 4
+#pragma unroll
                     for (int k = 0; k < D / 16; ++k) {
                         const uint32_t at = ((k >> 2) * 16384 + (k & 3) * 32) >> 4;
-                        tc_mma_f16(tm + 128 * t, qd + at, kd + at, kScoreDesc, k ? 1u : 0u);
+                        tc_mma_f16(tm + 64 * half, qd + at, kd + at, kScoreDesc, k ? 1u : 0u);
                     }
-                    mbar_arrive(&sm.s_full[t]);  // what this thread has seen (the block's references) goes on with it
-                    tc_commit(&sm.s_full[t]);
-                    if (t == 1) tc_commit(&sm.k_free[j & 1]);
+                    mbar_arrive(&sm.s_full[t][half]);  // what this thread has seen (the block's references) goes on with it
+                    tc_commit(&sm.s_full[t][half]);
+                    if (half == 1) tc_commit(&sm.k_free[b & 1]);
+                }
+                __syncwarp();
+            }
+            if (h > 0) {  // O (+)= P V of the half before
+                const int b = j + ((h - 1) >> 1), half = (h - 1) & 1;
+                if (half == 0 && !warp_wait(&sm.v_full[b & 1], (b >> 1) & 1, &sm.abort)) return;
+                if (!warp_wait(&sm.p_full[t][half], b & 1, &sm.abort)) return;
+                tc_fence_after();
+                const uint64_t vd = v0 + (b & 1) * kNext + half * kHalf;
+                if (elect_one()) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        tc_mma_f16_ts(tm + 256, tm + 64 * half + 8 * k, vd + (k * 2048 >> 4), kValueDesc, h == 1 && k == 0 ? 0u : 1u);
+                    tc_commit(&sm.o_done[t]);
+                    if (h == halves) tc_commit(&sm.o_full[t]);
+                    if (half == 1) tc_commit(&sm.v_free[b & 1]);
                 }
                 __syncwarp();
             }
         }
-#pragma unroll 1
-        for (int t = 0; t < 2; ++t) {
-            if (!values(t, j - 1, n == 1)) return;
-            if (elect_one()) {
-                tc_commit(&sm.o_full[t]);
-                if (t == 1) tc_commit(&sm.v_free[(j - 1) & 1]);
-            }
-            __syncwarp();
-        }
-        ++units;
+        j += halves >> 1;
     }
 }
 
@@ -1232,26 +1222,29 @@ __device__ __forceinline__ void many_softmax(const AttendParams& p, ManyShared<D
         }
         if (!more) return;
         ref = 0.0f, bound = -INFINITY, sum = 0.0f, vref = 0;
-        const int begin = unit.begin, end = unit.end;
-        for (int block = begin; block < end; ++block, ++j) {
-            if (!warp_wait(&sm.r_full[j & 3], (j >> 2) & 1, &sm.abort)) return;
-            if (!warp_wait(&sm.s_full[t], j & 1, &sm.abort)) return;
+        const int begin = unit.begin, halves = 2 * (unit.end - unit.begin);
+#pragma unroll 1
+        for (int h = 0; h < halves; ++h) {  // 64 keys
+            const int b = j + (h >> 1), half = h & 1;
+            const uint32_t th = ts + 64 * half;
+            if (half == 0 && !warp_wait(&sm.r_full[b & 3], (b >> 2) & 1, &sm.abort)) return;
+            if (!warp_wait(&sm.s_full[t][half], b & 1, &sm.abort)) return;
             tc_fence_after();
-            float f[4];
+            float f[2];
             uint32_t gone = 0;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < 2; ++i) {
                 // score of a product: times 2^(k_ref - 127 - kOperandLift)
-                f[i] = fmaxf(row.factor * __uint_as_float(static_cast<uint32_t>(max(sm.k_ref[j & 3][i] - kOperandLift, 1)) << 23),
-                             1.17549435e-38f);
-                gone |= static_cast<uint32_t>(sm.gone[j & 3][i]) << (2 * i);
+                const int e = max(sm.k_ref[b & 3][2 * half + i] - kOperandLift, 1);
+                f[i] = fmaxf(row.factor * __uint_as_float(static_cast<uint32_t>(e) << 23), 1.17549435e-38f);
+                gone |= static_cast<uint32_t>(sm.gone[b & 3][2 * half + i]) << (2 * i);
             }
-            const int lo = row.lo - block * 128, hi = row.hi - block * 128;
-            if (__any_sync(0xFFFFFFFFu, gone != 0 || lo > 0 || hi < 127)) {  // masked in place
+            const int key0 = (begin * 2 + h) * 64, lo = row.lo - key0, hi = row.hi - key0;
+            if (__any_sync(0xFFFFFFFFu, gone != 0 || lo > 0 || hi < 63)) {  // masked in place
 #pragma unroll 1
-                for (int i = 0; i < 4; ++i) {
+                for (int i = 0; i < 2; ++i) {
                     uint32_t x[32];
-                    tmem_ld32(ts + 32 * i, x);
+                    tmem_ld32(th + 32 * i, x);
                     // columns lo .. hi, without those whose page is not there
                     const int a = max(lo - 32 * i, 0), z = min(hi - 32 * i, 31);
                     uint32_t keep = a > z ? 0u : (0xFFFFFFFFu << a) & (0xFFFFFFFFu >> (31 - z));
@@ -1259,20 +1252,18 @@ __device__ __forceinline__ void many_softmax(const AttendParams& p, ManyShared<D
                     tmem_ld_wait();
 #pragma unroll
                     for (int k = 0; k < 32; ++k) x[k] = (keep >> k) & 1 ? x[k] : 0xFF800000u;
-                    tmem_st16(ts + 32 * i, x);
-                    tmem_st16(ts + 32 * i + 16, x + 16);
+                    tmem_st16(th + 32 * i, x);
+                    tmem_st16(th + 32 * i + 16, x + 16);
                 }
                 tmem_st_wait();
             }
-            // The first 64 scores stay in registers, the others are read once for the maximum and again for their
-            // weights (which are written over the first 64 columns).
-            float s[128];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) tmem_ld32(ts + 32 * i, *reinterpret_cast<uint32_t(*)[32]>(s + 32 * i));
+            float s[64];
+            tmem_ld32(th, *reinterpret_cast<uint32_t(*)[32]>(s));
+            tmem_ld32(th + 32, *reinterpret_cast<uint32_t(*)[32]>(s + 32));
             tmem_ld_wait();
             float m = -INFINITY;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < 2; ++i) {
                 float a = fmax3(s[32 * i], s[32 * i + 1], s[32 * i + 2]), z = fmax3(s[32 * i + 16], s[32 * i + 17], s[32 * i + 18]);
 #pragma unroll
                 for (int k = 3; k < 15; k += 2) {
@@ -1282,7 +1273,7 @@ __device__ __forceinline__ void many_softmax(const AttendParams& p, ManyShared<D
                 a = fmax3(a, s[32 * i + 15], s[32 * i + 31]);
                 m = fmaxf(m, fmaxf(a, z) * f[i]);
             }
-            const int nv = sm.v_ref[j & 3];
+            const int nv = sm.v_ref[b & 3];
             if (__any_sync(0xFFFFFFFFu, m > bound || nv != vref)) {
                 float scale = nv - vref < 127 ? __uint_as_float(static_cast<uint32_t>(127 - (nv - vref)) << 23) : 0.0f;
                 vref = nv;
@@ -1294,7 +1285,9 @@ __device__ __forceinline__ void many_softmax(const AttendParams& p, ManyShared<D
                     sum *= shift;
                     scale *= shift;
                 }
-                if (block != begin) {
+                if (h > 0) {  // once the products of the half before are done (those of halves before that are: s_full)
+                    if (!warp_wait(&sm.o_done[t], (h - 1) & 1, &sm.abort)) return;
+                    tc_fence_after();
 #pragma unroll 1
                     for (int i = 0; i < D / 16; ++i) {
                         uint32_t o[16];
@@ -1308,30 +1301,25 @@ __device__ __forceinline__ void many_softmax(const AttendParams& p, ManyShared<D
             }
             float2 add[2] = {};
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if (i == 1) tmem_ld32(ts + 64, *reinterpret_cast<uint32_t(*)[32]>(s + 64));
-                if (i == 2) {
-                    tmem_ld_wait();
-                    tmem_ld32(ts + 96, *reinterpret_cast<uint32_t(*)[32]>(s + 96));
-                }
-                if (i == 3) tmem_ld_wait();
+            for (int i = 0; i < 2; ++i) {
                 const float2 f2 = make_float2(f[i], f[i]), r2 = make_float2(-ref, -ref);
-                uint32_t h[16];
+                uint32_t w[16];
 #pragma unroll
                 for (int k = 0; k < 16; ++k) {
                     float2 e = __ffma2_rn(make_float2(s[32 * i + 2 * k], s[32 * i + 2 * k + 1]), f2, r2);
                     e = make_float2(exp2_approx(e.x), exp2_approx(e.y));
                     add[k & 1] = __fadd2_rn(add[k & 1], e);
                     const __half2 y = __floats2half2_rn(e.x, e.y);
-                    h[k] = *reinterpret_cast<const uint32_t*>(&y);
+                    w[k] = *reinterpret_cast<const uint32_t*>(&y);
                 }
-                tmem_st16(ts + 16 * i, h);
+                tmem_st16(th + 16 * i, w);  // over scores that have been read
             }
             sum += (add[0].x + add[0].y) + (add[1].x + add[1].y);
             tmem_st_wait();
             tc_fence_before();
-            mbar_arrive(&sm.p_full[t]);
+            mbar_arrive(&sm.p_full[t][half]);
         }
+        j += halves >> 1;
     }
 }
 
@@ -1343,14 +1331,14 @@ __global__ void __launch_bounds__(kManyThreads, 1) attend_many_kernel(const __gr
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&sm.k_full[i], 128), mbar_init(&sm.k_free[i], 1);
-            mbar_init(&sm.v_full[i], 128), mbar_init(&sm.v_free[i], 1);
-            mbar_init(&sm.q_full[i], 128), mbar_init(&sm.s_full[i], 2);
-            mbar_init(&sm.p_full[i], 128), mbar_init(&sm.o_full[i], 1);
+            mbar_init(&sm.k_full[i], 128), mbar_init(&sm.k_free[i], 2);
+            mbar_init(&sm.v_full[i], 128), mbar_init(&sm.v_free[i], 2);
+            mbar_init(&sm.q_full[i], 128), mbar_init(&sm.o_done[i], 1), mbar_init(&sm.o_full[i], 1);
+            for (int h = 0; h < 2; ++h) mbar_init(&sm.s_full[i][h], 2), mbar_init(&sm.p_full[i][h], 128);
         }
         for (int i = 0; i < 4; ++i) mbar_init(&sm.r_full[i], 1);
-        mbar_init(&sm.drained, 1);
-        for (int i = 0; i < kManyUnits; ++i) mbar_init(&sm.unit_full[i], 1), mbar_init(&sm.unit_free[i], 17);
+        mbar_init(&sm.drained[0], 1), mbar_init(&sm.drained[1], 1);
+        for (int i = 0; i < kManyUnits; ++i) mbar_init(&sm.unit_full[i], 1), mbar_init(&sm.unit_free[i], 18);
         sm.abort = 0;
         fence_mbar_init();
     }
@@ -1376,13 +1364,14 @@ __global__ void __launch_bounds__(kManyThreads, 1) attend_many_kernel(const __gr
     } else {
         setmaxnreg_dec<kIssueRegs>();
         if (warp == 17) many_units<D>(p, sm, place, lane);
-        if (warp == 16) {
-            many_products<D>(sm, lane);
+        if (warp == 16 || warp == 18) {
+            const int t = (warp - 16) >> 1;
+            many_products<D>(sm, t, lane);
             __syncwarp();
             if (elect_one()) {
                 int gave_up = 0;  // nothing is in flight when tensor memory is given back, whatever happened
-                tc_commit(&sm.drained);
-                mbar_wait(&sm.drained, 0, &gave_up);
+                tc_commit(&sm.drained[t]);
+                mbar_wait(&sm.drained[t], 0, &gave_up);
             }
         }
         __syncwarp();
