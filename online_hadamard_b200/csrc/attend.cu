@@ -778,6 +778,12 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int* a
     return true;
 }
 
+// One arrival for what all lanes have done (32 of them would queue up at the barrier).
+__device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar);
+}
+
 // A warp's next unit: waits for number n, and gives number n - 1 back first.  False: there is none.
 template <int D>
 __device__ __forceinline__ bool next_unit(ManyShared<D>& sm, int n, int lane) {
@@ -959,7 +965,7 @@ __device__ __forceinline__ void many_keys(const AttendParams& p, ManyShared<D>& 
             }
         }
         fence_proxy_async_smem();
-        mbar_arrive(&sm.k_full[stage]);
+        warp_arrive(&sm.k_full[stage], lane);
     }
     cp_async_wait<0>();
 }
@@ -1043,7 +1049,7 @@ __device__ __forceinline__ void many_values(const AttendParams& p, ManyShared<D>
             }
         }
         fence_proxy_async_smem();
-        mbar_arrive(&sm.v_full[stage]);
+        warp_arrive(&sm.v_full[stage], lane);
     }
     cp_async_wait<0>();
 }
@@ -1158,7 +1164,7 @@ __device__ __forceinline__ QueryRow load_query(const AttendParams& p, ManyShared
         }
     }
     fence_proxy_async_smem();
-    mbar_arrive(&sm.q_full[t]);
+    warp_arrive(&sm.q_full[t], tid & 31);
     return q;
 }
 
@@ -1317,7 +1323,7 @@ __device__ __forceinline__ void many_softmax(const AttendParams& p, ManyShared<D
             sum += (add[0].x + add[0].y) + (add[1].x + add[1].y);
             tmem_st_wait();
             tc_fence_before();
-            mbar_arrive(&sm.p_full[t][half]);
+            warp_arrive(&sm.p_full[t][half], tid & 31);
         }
         j += halves >> 1;
     }
@@ -1331,10 +1337,10 @@ __global__ void __launch_bounds__(kManyThreads, 1) attend_many_kernel(const __gr
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&sm.k_full[i], 128), mbar_init(&sm.k_free[i], 2);
-            mbar_init(&sm.v_full[i], 128), mbar_init(&sm.v_free[i], 2);
-            mbar_init(&sm.q_full[i], 128), mbar_init(&sm.o_done[i], 1), mbar_init(&sm.o_full[i], 1);
-            for (int h = 0; h < 2; ++h) mbar_init(&sm.s_full[i][h], 2), mbar_init(&sm.p_full[i][h], 128);
+            mbar_init(&sm.k_full[i], 4), mbar_init(&sm.k_free[i], 2);
+            mbar_init(&sm.v_full[i], 4), mbar_init(&sm.v_free[i], 2);
+            mbar_init(&sm.q_full[i], 4), mbar_init(&sm.o_done[i], 1), mbar_init(&sm.o_full[i], 1);
+            for (int h = 0; h < 2; ++h) mbar_init(&sm.s_full[i][h], 2), mbar_init(&sm.p_full[i][h], 4);
         }
         for (int i = 0; i < 4; ++i) mbar_init(&sm.r_full[i], 1);
         mbar_init(&sm.drained[0], 1), mbar_init(&sm.drained[1], 1);
