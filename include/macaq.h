@@ -412,13 +412,15 @@ int macaq_kv4_gather(const uint8_t* cache, int64_t num_pages, int page_size, int
 /*
  * macaq_kv4_attention -- attention of query rows over the cache, o = softmax(scale q k^T) v.
  *   q        in   bf16 [T] rows of Hq heads, ldq elements apart (after norm and rotation)
- *   tables   in   int32 [B][table_width]: the pages of each sequence in order
+ *   tables   in   int32 [B][table_width]: the pages of each sequence in order (at most 2^30 keys); entries
+ *                 behind a sequence's last page, or of pages that lie before its windows, are not read
  *   kv_lens  in   int32 [B]: the keys of each sequence, its newest queries' own keys included
  *   cu_q     in   int32 [B + 1]: sequence b's queries are rows cu_q[b] .. cu_q[b+1] - 1, its last tokens:
  *                 query i of n stands at position kv_len - n + i.  NULL: one query per sequence, row b
  *                 (B = T, max_q = 1)
- *   max_q    in   the most queries of any sequence, known on the host; it picks the kernels.  A longer
- *                 sequence's rows past it are not written (MACAQ_EINDEX)
+ *   max_q    in   the most queries of any sequence, known on the host (< 2^21; it picks the kernels and their
+ *                 split, so one far too large costs time).  A longer sequence's rows past it are not
+ *                 written (MACAQ_EINDEX)
  *   scale    in   finite and > 0;  window in: 0, or the number of newest keys a query sees, its own included
  *   out      out  bf16 [T][Hq][D]; rows outside every sequence are left as they were
  *   lse      out  fp32 [T][Hq], the natural logarithm of the sum of exp(scale q k); NULL: not wanted

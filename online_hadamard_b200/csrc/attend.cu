@@ -658,7 +658,8 @@ __device__ __forceinline__ void few_unit(const AttendParams& p, FewShared<D, NT>
             float t = sum[n][e];
 #pragma unroll
             for (int x = 4; x < 32; x <<= 1) t += __shfl_xor_sync(0xFFFFFFFFu, t, x);
-            if (g == 0) sm.ml[warp][2 * c + e] = make_float2(bound[n][e] == -INFINITY ? -INFINITY : ref[n][e], t);
+            // (nothing seen: no reference and no sum; the sum of a row that is not finite is NaN)
+            if (g == 0) sm.ml[warp][2 * c + e] = make_float2(bound[n][e] == -INFINITY && t == 0.0f ? -INFINITY : ref[n][e], t);
 #pragma unroll
             for (int j = 0; j < 2 * kBlocks; ++j) {
                 float* row = joined + (warp * 8 + 2 * c + e) * D + 16 * j + 4 * g - (j & 1) * 14;
@@ -1191,7 +1192,7 @@ __device__ __forceinline__ void many_softmax(const AttendParams& p, ManyShared<D
             tc_fence_after();
             const float inv = sum > 0.0f ? 1.0f / sum : sum == 0.0f ? 0.0f : sum;
             const float vs = vref > kOperandLift ? __uint_as_float(static_cast<uint32_t>(vref - kOperandLift) << 23) : 0.0f;
-            const float m = bound == -INFINITY ? -INFINITY : ref;
+            const float m = bound == -INFINITY && sum == 0.0f ? -INFINITY : ref;  // (a row that is not finite: NaN)
             const int64_t at = out_slot * kManyRows + 128 * t + tid;
 #pragma unroll 1
             for (int b = 0; b < D / 32; ++b) {
@@ -1486,17 +1487,22 @@ __global__ void __launch_bounds__(128) attend_join_kernel(const __grid_constant_
 constexpr int64_t kMaxKeys = int64_t{1} << 30;  // of a sequence: positions and block ends stay in 32 bits
 
 // How a call is split, from what the host knows (not the sequences' lengths).
-constexpr int kFewMost = 64;  // query rows of a unit up to which attend_few_kernel is used
+// Query rows of a unit up to which attend_few_kernel is used.  Above, its tiles of 32 rows would read the keys
+// again for each (24 sequences of 4000 keys, 8 heads of 128: 64 rows 202 us, 144 us with one tile of 256); at 32
+// rows it is ahead at long contexts (118 against 142 us; heads of 64 67 against 125 us), behind at short ones (300
+// keys: 99 against 67 us).
+constexpr int kFewMost = 32;
 struct AttendPlan {
     int tile_rows, row_tiles, ctas, unit_cost;
     int64_t units;
     size_t bytes;
 };
 static AttendPlan plan_attend(int64_t B, int Hq, int Hk, int D, int64_t max_q) {
-    AttendPlan a;
+    AttendPlan a = {};
     const int64_t rows = max_q * (Hq / Hk);
     a.tile_rows = rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= kFewMost ? 32 : kManyRows;
     a.row_tiles = static_cast<int>((rows + a.tile_rows - 1) / a.tile_rows);
+    if (B > kMaxDim / (static_cast<int64_t>(Hk) * a.row_tiles)) return a;  // units are counted in 31 bits
     a.units = B * Hk * a.row_tiles;
     if (a.tile_rows == kManyRows) {
         a.ctas = sm_count();
@@ -1545,9 +1551,7 @@ static int launch_many(const AttendParams& p, cudaStream_t stream) {
 
 template <int D>
 static int launch_attend(const AttendParams& p, int64_t units, cudaStream_t stream) {
-    const int64_t blocks = p.ctas ? p.ctas : units;
-    if (blocks > kMaxDim) return MACAQ_ESHAPE;
-    const auto n = static_cast<unsigned>(blocks);
+    const auto n = static_cast<unsigned>(p.ctas ? p.ctas : units);
     const int st = p.tile_rows == kManyRows ? launch_many<D>(p, stream)
                    : p.tile_rows == 8  ? launch_few<D, 1>(p, n, stream)
                    : p.tile_rows == 16 ? launch_few<D, 2>(p, n, stream)

@@ -108,3 +108,15 @@ def test_binding_refuses_host_tensors():
 
 def test_status_string_of_index_events():
     assert mq.status_str(-9).startswith("MACAQ_EINDEX")
+
+
+def test_attention_counts_stay_in_their_bits():
+    """Sizes whose work could not be counted are refused: queries, units, keys of a sequence."""
+    def need(T=8, B=8, Hq=64, Hk=8, D=128, max_q=1):
+        return lib().macaq_kv4_attention_workspace_bytes(T, B, Hq, Hk, D, max_q)
+    assert need() > 0 and need(max_q=1 << 20) > 0
+    assert need(max_q=1 << 21) == 0 and need(B=1 << 30) == 0 and need(B=1 << 20, max_q=1 << 20) == 0
+    assert need(Hq=65) == 0 and need(D=32) == 0 and need(max_q=0) == 0 and need(T=-1) == 0
+    ok = dict(q=FAKE, T=4, ldq=512, Hq=4, Hk=2, D=128, cache=FAKE, pages=4, page=16, tables=FAKE, B=2, width=(1 << 26) + 1)
+    assert lib().macaq_kv4_attention(P(ok["q"]), 4, 512, 4, 2, 128, P(FAKE), 4, 16, P(FAKE), 2, ok["width"], P(FAKE),
+                                     P(FAKE), 3, 0.1, 0, P(FAKE), None, P(FAKE), 1 << 40, None) == -2
