@@ -55,7 +55,8 @@ struct HeadParams {
     int64_t num_pages;
     int page_size;
     const int64_t* slots;
-    int64_t head_blocks;  // CTAs of the head units; the rest hold the cache's blocks
+    int64_t head_blocks;   // CTAs of the head units
+    int64_t cache_blocks;  // CTAs of the cache's blocks, which come first: theirs is the longer work
 };
 
 __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
@@ -393,16 +394,16 @@ __device__ __forceinline__ void run_cache_blocks(const HeadParams& p, int64_t bl
 }
 
 template <int D, RopeMode MODE, bool CACHE>
-__global__ void __launch_bounds__(kHeadThreads) heads_kernel(const __grid_constant__ HeadParams p) {
+__global__ void __launch_bounds__(kHeadThreads, 8) heads_kernel(const __grid_constant__ HeadParams p) {
     griddep_launch_dependents();
     griddep_wait();  // the rows may be written, and the outputs read, by the preceding kernel
     if constexpr (CACHE) {
-        if (blockIdx.x >= p.head_blocks) {
-            run_cache_blocks<D>(p, blockIdx.x - p.head_blocks, MODE == RopeMode::kPair);
+        if (blockIdx.x < p.cache_blocks) {
+            run_cache_blocks<D>(p, blockIdx.x, MODE == RopeMode::kPair);
             return;
         }
     }
-    run_head_units<D, MODE>(p, blockIdx.x);
+    run_head_units<D, MODE>(p, blockIdx.x - p.cache_blocks);
 }
 
 // Eight E2M1 codes of a word (element j in nibble j) as floats.
@@ -576,7 +577,8 @@ extern "C" int macaq_kv4_append(const uint16_t* qkv, int64_t T, int64_t ld, int 
     if (!qkv || (Hq && !q) || !cache || !slots || (interleaved & ~1)) return MACAQ_EINVAL;
     split_heads(p, head_dim, false);
     const int64_t items = 2 * T * Hk * (head_dim / 32);
-    const int64_t blocks = p.head_blocks + (items + kHeadThreads - 1) / kHeadThreads;
+    p.cache_blocks = (items + kHeadThreads - 1) / kHeadThreads;
+    const int64_t blocks = p.cache_blocks + p.head_blocks;
     if (blocks > kMaxDim) return MACAQ_ESHAPE;
     const auto s = static_cast<cudaStream_t>(stream);
     return head_dim == 64 ? launch_heads<64, true>(p, interleaved, blocks, s)
