@@ -117,8 +117,9 @@ __device__ __forceinline__ Tile tile_of(const AttendParams& p, int64_t item, int
 // (i + 1) len), whatever units they belong to.  A unit that one CTA holds whole is written directly, parts of one
 // are joined by attend_join_kernel.  A CTA cuts at most two units: its parts go to slot 0 (the unit that its
 // range begins in) and slot 1 (the one it ends in).  No range is shorter than kMinKeys keys (joining would
-// cost more than it saves).
-constexpr int kMinKeys = 128;
+// cost more than it saves: one sequence of 30000 keys, 7 heads on one, takes 22.5, 17.6 and 16.3 us with 128, 256
+// and 512 keys; of 300 keys, 64 heads on 8, 11.7, 12.7 and 15.0 us).
+constexpr int kMinKeys = 256;
 __device__ __forceinline__ int64_t tile_places(const AttendParams& p, const Tile& t) {
     return t.nrows > 0 ? static_cast<int64_t>(t.blocks + p.unit_cost) * p.Hk : 0;
 }
@@ -379,15 +380,22 @@ __device__ __forceinline__ void few_unit(const AttendParams& p, FewShared<D, NT>
         fetch(i, pg);
     }
 
-    for (int r = warp; r < kRows; r += 4) {
-        const bool real = r < nrows;
-        const int qi = (r0 + r) / p.G;
+    uint16_t raw[kRows / 4][kBlocks];  // of all rows first: one wait for them
+#pragma unroll
+    for (int y = 0; y < kRows / 4; ++y) {
+        const int r = warp + 4 * y, qi = (r0 + r) / p.G;
         const uint16_t* src = p.q + (s.row0 + qi) * p.ldq + static_cast<int64_t>(kvh * p.G + (r0 + r) - qi * p.G) * D;
+#pragma unroll
+        for (int i = 0; i < kBlocks; ++i) raw[y][i] = r < nrows ? src[32 * i + lane] : 0;
+    }
+#pragma unroll
+    for (int y = 0; y < kRows / 4; ++y) {
+        const int r = warp + 4 * y, qi = (r0 + r) / p.G;
         float x[kBlocks];
         uint32_t top = 0;
 #pragma unroll
         for (int i = 0; i < kBlocks; ++i) {
-            const uint32_t w = real ? static_cast<uint32_t>(src[32 * i + lane]) << 16 : 0u;
+            const uint32_t w = static_cast<uint32_t>(raw[y][i]) << 16;
             x[i] = __uint_as_float(w);
             top = max(top, w & 0x7FFFFFFFu);
         }
@@ -399,7 +407,7 @@ __device__ __forceinline__ void few_unit(const AttendParams& p, FewShared<D, NT>
         if (lane == 0) {
             sm.factor[r] = score_factor(p.scale_log2, E);
             sm.lo[r] = first_key(p, s.pos0 + qi);
-            sm.hi[r] = real ? s.pos0 + qi : -1;
+            sm.hi[r] = r < nrows ? s.pos0 + qi : -1;
         }
     }
     __syncthreads();
@@ -1492,6 +1500,9 @@ constexpr int64_t kMaxKeys = int64_t{1} << 30;  // of a sequence: positions and 
 // rows it is ahead at long contexts (118 against 142 us; heads of 64 67 against 125 us), behind at short ones (300
 // keys: 99 against 67 us).
 constexpr int kFewMost = 32;
+// Keys of a sequence's table up to which few rows are not cut (one query, 64 heads on 8: 48 sequences of 500 keys 14.8
+// against 23.5 us, 32 of 1000 keys 19.9 against 23.9 us, one of 1000 keys 13.4 against 12.5 us).
+constexpr int64_t kWholeKeys = 1024;
 struct AttendPlan {
     int tile_rows, row_tiles, ctas, unit_cost;
     int64_t units;
@@ -1599,6 +1610,8 @@ extern "C" int macaq_kv4_attention(const uint16_t* q, int64_t T, int64_t ldq, in
     p.scale_log2 = scale * kLog2e, p.window = static_cast<int>(window < kMaxDim ? window : 0), p.out = out, p.lse = lse;
     p.tile_rows = plan.tile_rows, p.row_tiles = plan.row_tiles, p.ctas = plan.ctas;
     p.unit_cost = plan.unit_cost;
+    // few rows whose tables hold no more than kWholeKeys keys are not cut: reading the parts again costs more
+    if (p.tile_rows != kManyRows && table_width * page_size <= kWholeKeys) p.ctas = 0;
     p.cuts = static_cast<CutUnit*>(workspace);
     p.part_ml = reinterpret_cast<float2*>(p.cuts + p.ctas);
     p.part_o = reinterpret_cast<float*>(p.part_ml + static_cast<int64_t>(p.ctas) * 2 * p.tile_rows);
