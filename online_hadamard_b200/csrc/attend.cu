@@ -1495,11 +1495,14 @@ __global__ void __launch_bounds__(128) attend_join_kernel(const __grid_constant_
 constexpr int64_t kMaxKeys = int64_t{1} << 30;  // of a sequence: positions and block ends stay in 32 bits
 
 // How a call is split, from what the host knows (not the sequences' lengths).
-// Query rows of a unit up to which attend_few_kernel is used.  Above, its tiles of 32 rows would read the keys
-// again for each (24 sequences of 4000 keys, 8 heads of 128: 64 rows 202 us, 144 us with one tile of 256); at 32
-// rows it is ahead at long contexts (118 against 142 us; heads of 64 67 against 125 us), behind at short ones (300
-// keys: 99 against 67 us).
+// attend_few_kernel takes up to 16 query rows of a unit always, and up to kFewMost where tables are longer than
+// kWholeKeys keys and, for heads of 128, there are kFewUnits pairs of a sequence and a kv head: its 32-row tiles
+// are bound by latency, the tiles of 256 of attend_many_kernel by the empty rows.  Measured, 32 rows (4 queries, 8
+// heads a kv head, 8 kv heads), few against many: heads of 128, 4000 keys, 8 sequences 73 / 64 us, 16 96 / 105 us,
+// 24 118 / 142 us; 64 of 300 keys 99 / 65 us; heads of 64, 4000 keys, 8 sequences 44 / 58 us.  64 rows (24 sequences
+// of 4000 keys, tiles of 32 read the keys twice): 202 / 144 us.
 constexpr int kFewMost = 32;
+constexpr int kFewUnits = 96;
 // Keys of a sequence's table up to which few rows are not cut (one query, 64 heads on 8: 48 sequences of 500 keys 14.8
 // against 23.5 us, 32 of 1000 keys 19.9 against 23.9 us, one of 1000 keys 13.4 against 12.5 us).
 constexpr int64_t kWholeKeys = 1024;
@@ -1508,10 +1511,11 @@ struct AttendPlan {
     int64_t units;
     size_t bytes;
 };
-static AttendPlan plan_attend(int64_t B, int Hq, int Hk, int D, int64_t max_q) {
+static AttendPlan plan_attend(int64_t B, int Hq, int Hk, int D, int64_t max_q, int64_t keys) {
     AttendPlan a = {};
     const int64_t rows = max_q * (Hq / Hk);
-    a.tile_rows = rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= kFewMost ? 32 : kManyRows;
+    const bool few32 = rows <= kFewMost && keys > kWholeKeys && (D == 64 || B * Hk >= kFewUnits);
+    a.tile_rows = rows <= 8 ? 8 : rows <= 16 ? 16 : few32 ? 32 : kManyRows;
     a.row_tiles = static_cast<int>((rows + a.tile_rows - 1) / a.tile_rows);
     if (B > kMaxDim / (static_cast<int64_t>(Hk) * a.row_tiles)) return a;  // units are counted in 31 bits
     a.units = B * Hk * a.row_tiles;
@@ -1520,7 +1524,7 @@ static AttendPlan plan_attend(int64_t B, int Hq, int Hk, int D, int64_t max_q) {
         a.unit_cost = 4;
     } else {  // cut while there are few units: many balance themselves, and need no joining
         const int resident = sm_count() * few_resident(a.tile_rows / 8);
-        a.ctas = a.units >= 4 * resident ? 0 : resident;
+        a.ctas = a.units >= 4 * resident || keys <= kWholeKeys ? 0 : resident;
         a.unit_cost = 16;
     }
     a.bytes = static_cast<size_t>(a.ctas) * (2 * a.tile_rows * (static_cast<size_t>(D) * 4 + 8) + sizeof(CutUnit));
@@ -1580,7 +1584,10 @@ extern "C" size_t macaq_kv4_attention_workspace_bytes(int64_t T, int64_t B, int 
         Hq % Hk != 0 || max_q < 1 || max_q > kMaxDim / kMaxHeads)
         return 0;
     if (T == 0 || B == 0) return 256;
-    return plan_attend(B, Hq, Hk, head_dim, max_q).bytes;
+    // whatever the tables' width
+    const size_t a = plan_attend(B, Hq, Hk, head_dim, max_q, 0).bytes;
+    const size_t z = plan_attend(B, Hq, Hk, head_dim, max_q, kMaxKeys).bytes;
+    return a && z ? (a > z ? a : z) : 0;
 }
 
 extern "C" int macaq_kv4_attention(const uint16_t* q, int64_t T, int64_t ldq, int Hq, int Hk, int head_dim,
@@ -1602,7 +1609,7 @@ extern "C" int macaq_kv4_attention(const uint16_t* q, int64_t T, int64_t ldq, in
         (reinterpret_cast<uintptr_t>(cu_q) & 3u) || (reinterpret_cast<uintptr_t>(lse) & 3u))
         return MACAQ_EALIGN;
     if (workspace_bytes < need) return MACAQ_EWORKSPACE;
-    const AttendPlan plan = plan_attend(B, Hq, Hk, head_dim, max_q);
+    const AttendPlan plan = plan_attend(B, Hq, Hk, head_dim, max_q, table_width * page_size);
     AttendParams p = {};
     p.q = q, p.T = T, p.ldq = ldq, p.Hq = Hq, p.Hk = Hk, p.G = Hq / Hk, p.cache = cache, p.num_pages = num_pages;
     p.page_size = page_size, p.page_shift = __builtin_ctz(page_size), p.tables = tables, p.table_width = table_width;
@@ -1610,8 +1617,6 @@ extern "C" int macaq_kv4_attention(const uint16_t* q, int64_t T, int64_t ldq, in
     p.scale_log2 = scale * kLog2e, p.window = static_cast<int>(window < kMaxDim ? window : 0), p.out = out, p.lse = lse;
     p.tile_rows = plan.tile_rows, p.row_tiles = plan.row_tiles, p.ctas = plan.ctas;
     p.unit_cost = plan.unit_cost;
-    // few rows whose tables hold no more than kWholeKeys keys are not cut: reading the parts again costs more
-    if (p.tile_rows != kManyRows && table_width * page_size <= kWholeKeys) p.ctas = 0;
     p.cuts = static_cast<CutUnit*>(workspace);
     p.part_ml = reinterpret_cast<float2*>(p.cuts + p.ctas);
     p.part_o = reinterpret_cast<float*>(p.part_ml + static_cast<int64_t>(p.ctas) * 2 * p.tile_rows);
