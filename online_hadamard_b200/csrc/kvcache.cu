@@ -16,7 +16,10 @@
 // token's angles and the weights in registers.  Key and value heads bound for the cache: one thread
 // owns one 32-element block, so the whole transform and quantisation runs in its registers as in
 // quant.cu; the D / 32 threads of a head exchange their sums of squares and code words by shuffles.
-// Both are bound by the bytes of the rows (2 B an element in and out, 17/32 B into the cache).
+// Both are bound by the bytes of the rows (2 B an element in and out, 17/32 B into the cache).  4096 rows of
+// 64 + 8 heads of 128: norm and rotation 27.4 us (5.6 TB/s), with 8 value heads and the cache 37 us (4.2 TB/s: the
+// threads of the cache's blocks read and transform 64 bytes each, 1000 instructions), reading back 10.4 us.
+// 64 registers a thread: at 78 the append takes 40 us (30 % of the warps resident), at 48 43 us (spills).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
