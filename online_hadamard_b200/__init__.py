@@ -610,9 +610,9 @@ def kv4_page_bytes(page_size: int, head_dim: int) -> int:
 
 def _need_cache(cache, page_size: int, head_dim: int, device=None):
     """(pages, kv heads) of a cache tensor."""
-    pb = kv4_page_bytes(page_size, head_dim)
-    if pb == 0:
+    if page_size not in (16, 32, 64, 128) or head_dim not in (64, 128):
         raise ValueError(f"page_size must be 16, 32, 64 or 128 and head_dim 64 or 128, got {page_size}, {head_dim}")
+    pb = page_size * head_dim * 17 // 16  # kv4_page_bytes
     _need(cache, "cache", torch.uint8, device=device)
     if cache.dim() != 3 or cache.shape[2] != pb:
         raise ValueError(f"cache must have shape (pages, kv heads, {pb}), got {tuple(cache.shape)}")

@@ -392,7 +392,7 @@ __device__ __forceinline__ void few_unit(const AttendParams& p, FewShared<D, NT>
         const int r = warp + 4 * y, qi = (r0 + r) / p.G;
         const uint16_t* src = p.q + (s.row0 + qi) * p.ldq + static_cast<int64_t>(kvh * p.G + (r0 + r) - qi * p.G) * D;
 #pragma unroll
-        for (int i = 0; i < kBlocks; ++i) raw[y][i] = r < nrows ? src[32 * i + lane] : 0;
+        for (int i = 0; i < kBlocks; ++i) raw[y][i] = r < nrows ? __ldcg(src + 32 * i + lane) : 0;
     }
 #pragma unroll
     for (int y = 0; y < kRows / 4; ++y) {
@@ -1414,7 +1414,9 @@ __global__ void __launch_bounds__(kManyThreads, 1) attend_many_kernel(const __gr
 }
 
 // Joins the parts of the units that were cut: CTA (i, y) those of the unit that range i ends in.  SPREAD: row y, its
-// parts spread over the warps (few rows of many parts); otherwise a warp a row (many rows of two or three).
+// parts spread over the warps (few rows of many parts); otherwise a warp a row (many rows of two or three).  Parts are
+// read through L2: kernels of several calls may be resident at once (each waits for the one ahead), so a line of
+// the call before may have come to this SM's L1 after this grid was launched.
 template <int D, bool SPREAD>
 __global__ void __launch_bounds__(128) attend_join_kernel(const __grid_constant__ AttendParams p) {
     constexpr int kElems = D / 32, kWarps = SPREAD ? 4 : 1;  // elements of a lane, neighbours; warps of a row
@@ -1434,7 +1436,7 @@ __global__ void __launch_bounds__(128) attend_join_kernel(const __grid_constant_
     for (int base = k0; base < u.parts; base += 32 * kWarps) {  // up to 32 parts at a time, one a lane
         const int mine = base + kWarps * lane;
         float2 ml = make_float2(-INFINITY, 0.0f);
-        if (mine < u.parts) ml = p.part_ml[place_of(mine)];
+        if (mine < u.parts) ml = __ldcg(&p.part_ml[place_of(mine)]);
         float top = ml.x;
 #pragma unroll
         for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, x));
@@ -1453,9 +1455,9 @@ __global__ void __launch_bounds__(128) attend_join_kernel(const __grid_constant_
             const float* src = p.part_o + place_of(base + kWarps * k) * D + kElems * lane;
             float x[kElems];
             if constexpr (kElems == 4)
-                *reinterpret_cast<float4*>(x) = *reinterpret_cast<const float4*>(src);
+                *reinterpret_cast<float4*>(x) = __ldcg(reinterpret_cast<const float4*>(src));
             else
-                *reinterpret_cast<float2*>(x) = *reinterpret_cast<const float2*>(src);
+                *reinterpret_cast<float2*>(x) = __ldcg(reinterpret_cast<const float2*>(src));
             total += wk;
 #pragma unroll
             for (int j = 0; j < kElems; ++j) o[j] += wk == 0.0f ? 0.0f : wk * x[j];
