@@ -744,7 +744,7 @@ __global__ void __launch_bounds__(kFewThreads, few_resident(NT)) attend_few_kern
 // in halves of 64 keys: in tensor memory stand S_0, S_1 (two halves of 64 columns each, the first 32 of a half
 // then P) and O_0, O_1 (128 each), so that a half's scores are there before the softmax of the one ahead ends.
 // E2M1 times a power of two is exact in f16: K is held relative to the largest scale of a warp's 32 tokens (which
-// goes into those columns' score factor), V relative to a reference above the largest scale met (rescaled like
+// goes into those columns' score factor), V relative to a reference above the largest scale met in the unit (rescaled like
 // the softmax reference when it moves), with 2^12 on top, so scales down to 2^-26 of the largest are exact.
 //
 // Measured: a prompt of 8192 tokens, 32 heads of 128 on 8, 605 us, 910 TFLOP/s of the pairs the mask leaves (tensor
@@ -853,6 +853,7 @@ struct CodeStream {
     uint32_t there;   // strips of the pending request that were copied, that are seen
     uint32_t seen;
     int first, last;  // the tokens of the pending request that any row sees, relative to its first
+    bool fresh;       // it begins a unit
     int w, lane;
 
     __device__ __forceinline__ CodeStream(const AttendParams& p_, ManyShared<D>& sm_, int w_, int lane_)
@@ -909,6 +910,7 @@ struct CodeStream {
                                src + (IS_V ? lay.v_scales() : lay.k_scales()) + at * kBlocks + 16 * lane);
             }
             first = u0.t.sp.first_lo - t0, last = u0.t.sp.last_hi - t0;
+            fresh = block == u0.begin;
             if (++block == u0.end) begin_unit();
             look();
         }
@@ -1039,6 +1041,7 @@ __device__ __forceinline__ void many_values(const AttendParams& p, ManyShared<D>
                 top = max(top, byte_max(scale[i][r]));
             }
         }
+        if (cs.fresh) ref = 0;  // nothing of one unit's values reaches another's
         __syncwarp();
         pending = cs.more;
         cs.request(raw);

@@ -1,0 +1,116 @@
+"""Attention where the sizes of values or keys lie far apart: what one key, block or sequence holds must not take
+another's place.  Tolerances are relative to each row's own weighted values, for each block of 32 elements."""
+import numpy as np
+import pytest
+import torch
+
+from tests import kv_util as kv
+from tests.test_gpu_kv_attention import cuda, mq  # noqa: F401  (mq is a fixture)
+
+pytestmark = pytest.mark.gpu
+
+
+class Cached:
+    """Sequences given as (k [L, Hk, D], v, q [n, Hq, D]) in a cache of shuffled pages."""
+
+    def __init__(self, seqs, page, room=0, seed=0):
+        rng = np.random.default_rng(seed)
+        self.Hk, self.D = seqs[0][0].shape[1:]
+        self.Hq, self.page = seqs[0][2].shape[1], page
+        self.kv_lens = np.array([len(s[0]) for s in seqs], np.int32)
+        self.cu = np.concatenate(([0], np.cumsum([len(s[2]) for s in seqs]))).astype(np.int32)
+        self.max_q = max(len(s[2]) for s in seqs)
+        used = max(-(-int(n) // page) for n in self.kv_lens)
+        width = max(used, -(-room // page))
+        order = rng.permutation(len(seqs) * used).reshape(len(seqs), used)
+        self.tables = np.concatenate((order, np.full((len(seqs), width - used), -7)), 1).astype(np.int32)
+        self.cache = np.zeros((len(seqs) * used, self.Hk, kv.page_bytes(page, self.D)), np.uint8)
+        with np.errstate(invalid="ignore"):  # infinities
+            for b, (k, v, _) in enumerate(seqs):
+                j = np.arange(len(k))
+                kv.store(self.cache, order[b][j // page] * page + j % page, page, k, v)
+        self.q = np.concatenate([s[2] for s in seqs])
+        self.scale = self.D ** -0.5
+
+    def run(self, mq):
+        """out, fp64 on the host, and the logarithms of the sums."""
+        lse = torch.empty(self.q.shape[:2], dtype=torch.float32, device="cuda")
+        out = mq.macaq_kv4_attention(cuda(self.q, torch.bfloat16), cuda(self.cache), self.page, cuda(self.tables),
+                                     cuda(self.kv_lens), cuda(self.cu), max_q=self.max_q, lse=lse)
+        assert mq.macaq_device_status() == 0
+        return out, lse
+
+    def check(self, mq, rows=None, block_gain=None):
+        """Every element of the rows in `rows` (query index -> bool) against 64 bits.
+
+        A row's weights are off by factors 1 + eps_j: the transformed query is rounded to f16, which moves a score
+        by 2^-11 scale sum |q'_i k'_i|; fp32 rounds it by 2^-24 of itself a few times (2^-21 (1 + |s|)); the weight
+        is rounded to f16, 2^-11, and scaled in it.  With A_j = sum_i |v'_ji| / sqrt(32), what an element can take
+        from a unit of weight j, that moves an element by sum p_j eps_j A_j and, through the denominator, by
+        sum p_j eps_j sum p_j A_j.  Weights below f16's normal range are off by half of its smallest step instead, 2^-25,
+        where the largest weight is 2^6 or more: 2^-31 of it, in the kernel of few rows times scales that are at most 2^14
+        above the smallest in the same part, in the other times values at most 2^20 above it.  Sums are fp32, (n + 64)
+        roundings of 2^-24, and the result is rounded to bf16."""
+        got, lse = self.run(mq)
+        got, lse = got.double().cpu().numpy(), lse.double().cpu().numpy()
+        K, V = kv.decode(self.cache, self.page, self.D)
+        G, nb = self.Hq // self.Hk, self.D // 32
+        for b, L in enumerate(self.kv_lens):
+            j = np.arange(L)
+            at = self.tables[b][j // self.page]
+            n = int(self.cu[b + 1] - self.cu[b])
+            for i in range(n):
+                if rows is not None and not rows(i, n):
+                    continue
+                t, see = int(self.cu[b]) + i, j <= L - n + i
+                for h in range(self.Hq):
+                    k, v = K[at[see], h // G, j[see] % self.page], V[at[see], h // G, j[see] % self.page]
+                    q = self.q[t, h].astype(np.float64)
+                    qt, kt, vt = (np.abs(kv.hadamard(x.reshape(-1, nb, 32)) / np.sqrt(32.0)) for x in (q, k, v))
+                    s = k @ q * self.scale
+                    p = np.exp(s - s.max())
+                    top, p = p.max() / p.sum(), p / p.sum()
+                    ref = p @ v
+                    eps = 2.0 ** -11 * self.scale * (qt * kt).sum((1, 2)) + 2.0 ** -21 * (1 + np.abs(s)) + 2.0 ** -10
+                    A = vt.sum(-1) / np.sqrt(32.0)
+                    big = vt.max(-1)
+                    least = big[big > 0].min() if (big > 0).any() else 0.0
+                    weighted = p @ A
+                    tol = (p * eps) @ A + (p @ eps) * weighted + (len(p) + 64) * 2.0 ** -24 * weighted
+                    tol += 2.0 ** -31 * top * np.minimum(A, 2.0 ** 20 * least).sum(0)
+                    tol += len(p) * 2.0 ** -17 * 8.5 * top * least
+                    err = np.abs(got[t, h] - ref).reshape(nb, 32)
+                    bad = err > 2.0 ** -8 * np.abs(ref).reshape(nb, 32) + tol[:, None]
+                    assert not bad.any(), (b, i, h, err.max(-1), tol, np.abs(ref).reshape(nb, 32).max(-1))
+                    lref = s.max() + np.log(np.exp(s - s.max()).sum())
+                    assert abs(lse[t, h] - lref) <= p @ eps + 2.0 ** -16 * (1 + abs(lref))
+
+
+def sequence(rng, L, n, Hq, Hk, D, score=None):
+    """Random k, v and queries.  score: a key's score by its index, for queries that are all one direction."""
+    k, v = rng.standard_normal((2, L, Hk, D))
+    q = rng.standard_normal((n, Hq, D))
+    if score is not None:
+        u = rng.standard_normal(D)
+        q = u + 0.05 * q
+        for j, s in score.items():
+            k[j] = s * D ** 0.5 * u / (u @ u)
+    return kv.bf16(k), kv.bf16(v), kv.bf16(q)
+
+
+@pytest.mark.parametrize("nq,Hk", [(1, 2), (3, 2), (40, 2), (1, 40)])
+@pytest.mark.parametrize("gain", [2.0 ** 30, np.inf, np.nan])
+def test_other_sequences_keep_their_bits(mq, nq, Hk, gain):
+    """One sequence of a batch with huge or infinite values, others behind it on the same CTAs."""
+    rng = np.random.default_rng(54)
+    seqs = [sequence(rng, nq + 20, nq, 2 * Hk, Hk, 64) for _ in range(170 if Hk == 2 else 60)]
+    want, wl = Cached(seqs, 16).run(mq)
+    bad = range(0, len(seqs), 17)
+    for b in bad:
+        seqs[b][1][7, :, 9] *= np.float32(gain)
+        seqs[b][0][4, 0, 5] *= np.float32(gain)
+    out, lse = Cached(seqs, 16).run(mq)
+    same = torch.ones(len(out), dtype=torch.bool)
+    for b in bad:
+        same[b * nq:(b + 1) * nq] = False
+    assert torch.equal(out[same], want[same]) and torch.equal(lse[same], wl[same])
