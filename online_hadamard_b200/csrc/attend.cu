@@ -248,6 +248,12 @@ __device__ __forceinline__ float warp_fwht32(float x, int l) {
 constexpr float kSlack = 8.0f;
 constexpr float kLift = 6.0f;
 
+// Where V's scales lie too far apart for f16, weights times scales are bf16, whose exponents are fp32's, relative to
+// a reference 2^70 below the largest scale of the same 32 elements: 2^70, times 6, a weight of 2^14 and 2^30 keys, stays
+// below 2^118, and scales down to 2^-196 of the largest are not lost beside it (an infinity is stored as 2^126, so values
+// of 2^-70 count even there).
+__device__ __forceinline__ int wide_reference(int top) { return max(top - 70, 1); }
+
 // --------------------------------------------------------------------------- few query rows
 //
 // CTAs of 4 warps.  A warp takes blocks of 32 tokens, as two strips of 16: S^T = K Q^T (m = 16 tokens,
@@ -263,7 +269,14 @@ constexpr float kLift = 6.0f;
 // instructions (a conversion per two codes, 64, and 32 matrix instructions and their scales among them); they fill 56 %
 // of the issue slots of three CTAs an SM.  Four CTAs (128 registers, spilling) issue no more; one strip at a time
 // is 9 % slower, as two in flight hide each other's latencies; a CTA's start and end cost some 15 us in all.
+//
+// V's scale as the exponent of an f16 reaches down to 2^-14 of the reference, which stands up to 2^3 above the largest scale
+// met.  A warp notes the smallest it met, too; where that lies lower (V blocks 2^11 to 2^14 and more apart, and it does
+// not matter which row sees them) the CTA does the unit again, WIDE: weights and scales as bf16, the weights as a sum of
+// two (2^-17 of themselves), relative to a reference of each block of elements.  That is twice the matrix
+// instructions for V and some more for its codes.
 constexpr int kFewThreads = 128;
+constexpr int kFewSpan = 14;
 constexpr int kStages = 3;
 constexpr int kFewShift = 5;
 
@@ -289,7 +302,7 @@ struct FewShared {
     alignas(16) uint8_t ring[kRing > kJoin ? kRing : kJoin];  // in the end the warps' sums of 8 rows
     struct Scales {
         alignas(16) float k[4][2][16][kBlocks];    // a warp's strips: 2^(e - 127) of K's blocks
-        alignas(16) uint32_t v[4][2][8][kBlocks];  // f16 2^(e - vref) of V's, two tokens
+        alignas(16) uint32_t v[4][2][8][kBlocks];  // f16 (WIDE: bf16) 2^(e - reference) of V's, two tokens
     };
     struct Both {
         Scales scale;
@@ -303,19 +316,21 @@ struct FewShared {
     float factor[8 * NT];
     int lo[8 * NT], hi[8 * NT];
     float2 ml[4][8];
-    float vref[4];
+    float vref[4][kBlocks];  // what a warp's sums of a block are relative to
+    int vtop[4][kBlocks];    // the largest scale that a warp met there
     PlaceShared place;
 };
 
-template <int D, int NT>
-__device__ __forceinline__ void few_unit(const AttendParams& p, FewShared<D, NT>& sm, const Unit& unit) {
+// One unit, or a CTA's part of it.  False, and nothing written, where V's scales lie too far apart for f16 (not WIDE).
+template <int D, int NT, bool WIDE>
+__device__ __forceinline__ bool few_unit(const AttendParams& p, FewShared<D, NT>& sm, const Unit& unit) {
     const Sequence& s = unit.t.s;
     const Span& sp = unit.t.sp;
     const int kvh = unit.kvh, r0 = unit.t.r0, nrows = unit.t.nrows, begin = unit.begin, end = unit.end;
     const int64_t slot = unit.slot;
     using S = TokenBlock<D>;
     constexpr int kBlocks = D / 32, kRows = 8 * NT;
-    constexpr int kSub = NT == 4 ? 1 : 2;  // strips worked on together, as registers allow
+    constexpr int kSub = NT == 4 || WIDE ? 1 : 2;  // strips worked on together, as registers allow
     const int lane = threadIdx.x & 31, warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0);
     const int g = lane >> 2, c = lane & 3;
     const int count = max(0, (end - begin - warp + 3) >> 2);  // blocks of this warp
@@ -427,7 +442,10 @@ __device__ __forceinline__ void few_unit(const AttendParams& p, FewShared<D, NT>
     }
     float f[NT][2], ref[NT][2], bound[NT][2], sum[NT][2], o[NT][2 * kBlocks][4];
     const int vp = D == 128 ? lane >> 2 : (lane >> 1) & 7, vb = lane & (kBlocks - 1);
-    int vref = 0;  // above the largest V scale met, which the sums are relative to
+    // V's scales: above the largest met, which the sums are relative to (WIDE: of the lane's block); the largest this lane
+    // met; the smallest but 0, less 1, in either half
+    int vref = WIDE ? wide_reference(sm.vtop[warp][vb]) : 0, vtop = 0;
+    uint32_t vlow = 0xFFFFFFFFu;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -543,11 +561,18 @@ __device__ __forceinline__ void few_unit(const AttendParams& p, FewShared<D, NT>
                     if (gone || t + 1 < sp.first_lo || t + 1 > sp.last_hi) ve[u][1] = 0;
                 }
             }
-            int vmax = max(ve[0][0], ve[0][1]);
-            if constexpr (kSub == 2) vmax = max(vmax, max(ve[1][0], ve[1][1]));
+            uint32_t v2[kSub];
+#pragma unroll
+            for (int u = 0; u < kSub; ++u) {
+                v2[u] = static_cast<uint32_t>(ve[u][0] | ve[u][1] << 16);
+                if constexpr (!WIDE) {
+                    vtop = max(max(ve[u][0], ve[u][1]), vtop);
+                    vlow = __viaddmin_u16x2(v2[u], 0xFFFFFFFFu, vlow);
+                }
+            }
 
             float top[NT][2];
-            bool grow = vmax > vref;
+            bool grow = !WIDE && vtop > vref;
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -560,8 +585,8 @@ __device__ __forceinline__ void few_unit(const AttendParams& p, FewShared<D, NT>
             }
             if (__any_sync(0xFFFFFFFFu, grow)) {
                 float vf = 1.0f;
-                const int nv = static_cast<int>(__reduce_max_sync(0xFFFFFFFFu, static_cast<unsigned>(vmax)));
-                if (nv > vref) {  // with room for three doublings before the next time
+                const int nv = WIDE ? 0 : static_cast<int>(__reduce_max_sync(0xFFFFFFFFu, static_cast<unsigned>(vtop)));
+                if (!WIDE && nv > vref) {  // with room for three doublings before the next time
                     const int to = min(nv + 3, 254);
                     vf = to - vref < 127 ? __uint_as_float(static_cast<uint32_t>(127 - (to - vref)) << 23) : 0.0f;
                     vref = to;
@@ -588,19 +613,19 @@ __device__ __forceinline__ void few_unit(const AttendParams& p, FewShared<D, NT>
                 }
             }
 
-            // exponent field e - vref + 15 of two tokens, 0 below it
-            const uint32_t k2 = static_cast<uint32_t>((15 - vref) & 0xFFFF) * 0x00010001u;
+            // exponent field e - vref + 15 (bf16: 127) of two tokens, 0 below it
+            const uint32_t k2 = static_cast<uint32_t>(((WIDE ? 127 : 15) - vref) & 0xFFFF) * 0x00010001u;
 #pragma unroll
             for (int u = 0; u < kSub; ++u)
                 sm.u.scale.v[warp][half + u][vp][vb] =
-                    __viaddmin_s16x2_relu(static_cast<uint32_t>(ve[u][0] | ve[u][1] << 16), k2, 0x000F000Fu) << 10;
+                    WIDE ? __viaddmin_s16x2_relu(v2[u], k2, 0x00FE00FEu) << 7 : __viaddmin_s16x2_relu(v2[u], k2, 0x000F000Fu) << 10;
             __syncwarp();
 
 #pragma unroll
             for (int u = 0; u < kSub; ++u) {
                 const uint8_t* st = st0 + (half + u) * S::kStrip;
                 // softmax weights, transposed into fragments: tokens 2c, 2c + 1 (2c + 8, 2c + 9) of row g
-                uint32_t pt0[NT], pt1[NT];
+                uint32_t pt0[NT], pt1[NT], pl0[NT], pl1[NT];  // (pl: what bf16 leaves of the weights)
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
                     const float e0 = exp2_approx(fmaf(sc[u][n][0], f[n][0], -ref[n][0]));
@@ -608,9 +633,15 @@ __device__ __forceinline__ void few_unit(const AttendParams& p, FewShared<D, NT>
                     const float e2 = exp2_approx(fmaf(sc[u][n][2], f[n][0], -ref[n][0]));
                     const float e3 = exp2_approx(fmaf(sc[u][n][3], f[n][1], -ref[n][1]));
                     sum[n][0] += e0 + e2, sum[n][1] += e1 + e3;
-                    const __half2 a = __floats2half2_rn(e0, e1), z = __floats2half2_rn(e2, e3);
-                    pt0[n] = movmatrix_trans(*reinterpret_cast<const uint32_t*>(&a));
-                    pt1[n] = movmatrix_trans(*reinterpret_cast<const uint32_t*>(&z));
+                    if constexpr (WIDE) {
+                        const uint32_t a = pack_bf16(e0, e1), z = pack_bf16(e2, e3);
+                        pt0[n] = movmatrix_trans(a), pl0[n] = movmatrix_trans(pack_bf16(e0 - bf_lo(a), e1 - bf_hi(a)));
+                        pt1[n] = movmatrix_trans(z), pl1[n] = movmatrix_trans(pack_bf16(e2 - bf_lo(z), e3 - bf_hi(z)));
+                    } else {
+                        const __half2 a = __floats2half2_rn(e0, e1), z = __floats2half2_rn(e2, e3);
+                        pt0[n] = movmatrix_trans(*reinterpret_cast<const uint32_t*>(&a));
+                        pt1[n] = movmatrix_trans(*reinterpret_cast<const uint32_t*>(&z));
+                    }
                 }
                 uint32_t va[4], vz[4];  // pairs c and c + 4: (first token: blocks 01, 23), (second token: 01, 23)
                 uint32_t vx0[kBlocks], vx1[kBlocks];
@@ -643,16 +674,32 @@ __device__ __forceinline__ void few_unit(const AttendParams& p, FewShared<D, NT>
                     uint32_t ea[4], oa[4], ez[4], oz[4];
                     e2m1x8_to_f16(ae, ea), e2m1x8_to_f16(ao, oa);
                     e2m1x8_to_f16(ze, ez), e2m1x8_to_f16(zo, oz);
+                    if constexpr (WIDE) {
+#pragma unroll
+                        for (int y = 0; y < 4; ++y) {
+                            ea[y] = e2m1_f16_to_bf16(ea[y]), oa[y] = e2m1_f16_to_bf16(oa[y]);
+                            ez[y] = e2m1_f16_to_bf16(ez[y]), oz[y] = e2m1_f16_to_bf16(oz[y]);
+                        }
+                    }
 #pragma unroll
                     for (int y = 0; y < 2; ++y) {
                         const int j = 2 * h + y;
 #pragma unroll
                         for (int n = 0; n < NT; ++n) {
-                            const __half2 b0 = __hmul2(*reinterpret_cast<const __half2*>(&pt0[n]), *reinterpret_cast<const __half2*>(&vx0[j]));
-                            const __half2 b1 = __hmul2(*reinterpret_cast<const __half2*>(&pt1[n]), *reinterpret_cast<const __half2*>(&vx1[j]));
-                            const uint32_t u0 = *reinterpret_cast<const uint32_t*>(&b0), u1 = *reinterpret_cast<const uint32_t*>(&b1);
-                            mma_f16_16x8x16(o[n][2 * j], ea[2 * y], oa[2 * y], ez[2 * y], oz[2 * y], u0, u1);
-                            mma_f16_16x8x16(o[n][2 * j + 1], ea[2 * y + 1], oa[2 * y + 1], ez[2 * y + 1], oz[2 * y + 1], u0, u1);
+                            if constexpr (WIDE) {
+#pragma unroll
+                                for (int x = 0; x < 2; ++x) {
+                                    const uint32_t u0 = mul_bf16x2(x ? pl0[n] : pt0[n], vx0[j]), u1 = mul_bf16x2(x ? pl1[n] : pt1[n], vx1[j]);
+                                    mma_bf16_16x8x16(o[n][2 * j], ea[2 * y], oa[2 * y], ez[2 * y], oz[2 * y], u0, u1);
+                                    mma_bf16_16x8x16(o[n][2 * j + 1], ea[2 * y + 1], oa[2 * y + 1], ez[2 * y + 1], oz[2 * y + 1], u0, u1);
+                                }
+                            } else {
+                                const __half2 b0 = __hmul2(*reinterpret_cast<const __half2*>(&pt0[n]), *reinterpret_cast<const __half2*>(&vx0[j]));
+                                const __half2 b1 = __hmul2(*reinterpret_cast<const __half2*>(&pt1[n]), *reinterpret_cast<const __half2*>(&vx1[j]));
+                                const uint32_t u0 = *reinterpret_cast<const uint32_t*>(&b0), u1 = *reinterpret_cast<const uint32_t*>(&b1);
+                                mma_f16_16x8x16(o[n][2 * j], ea[2 * y], oa[2 * y], ez[2 * y], oz[2 * y], u0, u1);
+                                mma_f16_16x8x16(o[n][2 * j + 1], ea[2 * y + 1], oa[2 * y + 1], ez[2 * y + 1], oz[2 * y + 1], u0, u1);
+                            }
                         }
                     }
                 }
@@ -660,13 +707,25 @@ __device__ __forceinline__ void few_unit(const AttendParams& p, FewShared<D, NT>
         }
     }
     cp_async_wait<0>();
+    if constexpr (!WIDE) {
+        const int low = static_cast<int>(__reduce_min_sync(0xFFFFFFFFu, min(vlow & 0xFFFFu, vlow >> 16))) + 1;
+        if (__syncthreads_or(low < vref - kFewSpan)) {
+#pragma unroll
+            for (int x = kBlocks; x < 32; x <<= 1) vtop = max(vtop, __shfl_xor_sync(0xFFFFFFFFu, vtop, x));
+            if (lane < kBlocks) sm.vtop[warp][lane] = vtop;
+            __syncwarp();
+            return false;
+        }
+    } else {
+        __syncthreads();
+    }
 
     // join the warps, one n-tile (8 rows) at a time: warp w's sums of row r at joined[w][r][..]
     float* joined = reinterpret_cast<float*>(sm.ring);
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
         if (8 * n >= nrows) break;
-        __syncthreads();
+        if (n > 0) __syncthreads();
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             float t = sum[n][e];
@@ -680,7 +739,7 @@ __device__ __forceinline__ void few_unit(const AttendParams& p, FewShared<D, NT>
                 *reinterpret_cast<float2*>(row) = make_float2(o[n][j][e], o[n][j][2 + e]);
             }
         }
-        if (lane == 0) sm.vref[warp] = __uint_as_float(static_cast<uint32_t>(vref) << 23);
+        if (lane < kBlocks) sm.vref[warp][lane] = __uint_as_float(static_cast<uint32_t>(vref) << 23);
         __syncthreads();
         constexpr int kAtOnce = kFewThreads / D;
         const int d = threadIdx.x % D;
@@ -699,7 +758,7 @@ __device__ __forceinline__ void few_unit(const AttendParams& p, FewShared<D, NT>
             const float inv = total > 0.0f ? 1.0f / total : total == 0.0f ? 0.0f : total;
 #pragma unroll
             for (int k = 0; k < 4; ++k)  // divided first: the sums times a large scale might not fit
-                if (w[k] != 0.0f) x += joined[(k * 8 + r) * D + d] * (w[k] * inv) * sm.vref[k];
+                if (w[k] != 0.0f) x += joined[(k * 8 + r) * D + d] * (w[k] * inv) * sm.vref[k][d / 32];
             if (slot >= 0) {
                 const int64_t at = slot * p.tile_rows + 8 * n + r;
                 p.part_o[at * D + d] = x;
@@ -714,6 +773,7 @@ __device__ __forceinline__ void few_unit(const AttendParams& p, FewShared<D, NT>
         }
     }
     __syncthreads();
+    return true;
 }
 
 template <int D, int NT>
@@ -725,7 +785,8 @@ __global__ void __launch_bounds__(kFewThreads, few_resident(NT)) attend_few_kern
     const Place place = p.ctas ? find_place<kFewThreads>(p, kFewShift, blockIdx.x, sm.place) : Place{};
     Walk walk = p.ctas ? Walk(p, place) : Walk(blockIdx.x, p.Hk);
     Unit unit;
-    while (walk.next(p, kFewShift, unit)) few_unit<D, NT>(p, sm, unit);
+    while (walk.next(p, kFewShift, unit))
+        if (!few_unit<D, NT, false>(p, sm, unit)) few_unit<D, NT, true>(p, sm, unit);
     if (p.ctas && threadIdx.x == 0) p.cuts[blockIdx.x] = walk.cut;
 }
 

@@ -167,6 +167,22 @@ __device__ __forceinline__ void mma_f16_16x8x16_first(float (&d)[4], uint32_t a0
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
 }
 
+// D += A B as mma_f16_16x8x16, operands bf16.
+__device__ __forceinline__ void mma_bf16_16x8x16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                                 uint32_t b0, uint32_t b1) {
+    asm(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+
 // Transposes an 8 x 8 matrix of 16-bit elements held as mma fragments.
 __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
     uint32_t d;
@@ -190,6 +206,12 @@ __device__ __forceinline__ void e2m1x8_to_f16(uint32_t w, uint32_t (&h)[4]) {
         "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
         : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
         : "r"(w));
+}
+
+// Two f16 that came from E2M1 codes (one bit of mantissa) as bf16: the exponent's bits move to where bf16 has the low five
+// of its own, which is 2^-112 of the value.
+__device__ __forceinline__ uint32_t e2m1_f16_to_bf16(uint32_t h) {
+    return mul_bf16x2((h & 0x80008000u) | ((h >> 3) & 0x0FFF0FFFu), 0x77807780u);
 }
 
 // ----------------------------------------------------------------------- tcgen05 / TMEM

@@ -9,6 +9,10 @@ from tests.test_gpu_kv_attention import cuda, mq  # noqa: F401  (mq is a fixture
 
 pytestmark = pytest.mark.gpu
 
+# (D, query heads a kv head, queries a sequence, kv heads, page, keys the tables have room for): 8, 16 and 32 rows of the
+# kernel of few rows, tables that are cut and that are not
+KERNELS = [(128, 2, 3, 2, 32, 0), (64, 4, 4, 1, 16, 0), (128, 8, 2, 1, 64, 2000), (64, 8, 4, 1, 32, 2000)]
+
 
 class Cached:
     """Sequences given as (k [L, Hk, D], v, q [n, Hq, D]) in a cache of shuffled pages."""
@@ -96,6 +100,53 @@ def sequence(rng, L, n, Hq, Hk, D, score=None):
         for j, s in score.items():
             k[j] = s * D ** 0.5 * u / (u @ u)
     return kv.bf16(k), kv.bf16(v), kv.bf16(q)
+
+
+def earlier(i, n):
+    return i < n - 1
+
+
+@pytest.mark.parametrize("D,G,nq,Hk,page,room", KERNELS)
+@pytest.mark.parametrize("gain", [2.0 ** 11, 2.0 ** 16, 2.0 ** 30, 2.0 ** 70, np.inf, np.nan])
+def test_a_huge_value_that_earlier_queries_do_not_see(mq, D, G, nq, Hk, page, room, gain):
+    rng = np.random.default_rng(50)
+    seqs = [sequence(rng, L, min(nq, L), G * Hk, Hk, D) for L in (nq + 13, nq + 150)]
+    for k, v, q in seqs:
+        v[-1, :, 3] *= np.float32(gain)
+        v[-1, :, 40] *= np.float32(gain)
+    Cached(seqs, page, room).check(mq, None if np.isfinite(gain) else earlier)
+
+
+@pytest.mark.parametrize("D,G,nq,Hk,page,room", KERNELS)
+@pytest.mark.parametrize("gain", [2.0 ** 13, 2.0 ** 30, 2.0 ** 56])
+def test_a_huge_value_of_little_weight(mq, D, G, nq, Hk, page, room, gain):
+    """A score 40 below the others': nothing of its value at 2^13 and 2^30 times theirs, as much as theirs at 2^56."""
+    rng = np.random.default_rng(51)
+    L = nq + 140
+    k, v, q = sequence(rng, L, nq, G * Hk, Hk, D, {3: -20.0, **{j: 20.0 for j in range(4, 12)}})
+    v[3] *= np.float32(gain)
+    Cached([(k, v, q)], page, room).check(mq)
+
+
+@pytest.mark.parametrize("D,G,nq,Hk,page,room", KERNELS)
+@pytest.mark.parametrize("step", [13, 30])
+def test_blocks_of_a_head_far_apart(mq, D, G, nq, Hk, page, room, step):
+    rng = np.random.default_rng(52)
+    k, v, q = sequence(rng, nq + 90, nq, G * Hk, Hk, D)
+    v *= np.repeat(np.float32(2.0) ** (-step * np.arange(D // 32)), 32)
+    Cached([(k, v, q), sequence(rng, nq, nq, G * Hk, Hk, D)], page, room).check(mq)
+
+
+@pytest.mark.parametrize("D,G,nq,Hk,page,room", KERNELS)
+def test_values_that_grow_and_shrink_by_far(mq, D, G, nq, Hk, page, room):
+    """From 2^-30 to 2^30 along the keys and back, with the weight on either side, and some values of zero."""
+    rng = np.random.default_rng(53)
+    L = nq + 200
+    for s in (1, -1):
+        k, v, q = sequence(rng, L, nq, G * Hk, Hk, D, {j: (-10.0 if j < L // 2 else 10.0) for j in range(0, L, 3)})
+        v *= (np.float32(2.0) ** np.linspace(-30 * s, 30 * s, L))[:, None, None]
+        v[5] = v[L - 2] = 0
+        Cached([(k, kv.bf16(v), q)], page, room).check(mq)
 
 
 @pytest.mark.parametrize("nq,Hk", [(1, 2), (3, 2), (40, 2), (1, 40)])
