@@ -800,6 +800,7 @@ __global__ void __launch_bounds__(kFewThreads, few_resident(NT)) attend_few_kern
 //   warpgroup 2      K: codes to f16 in shared memory, K-major
 //   warpgroup 3      V: likewise, elements along the rows (MN-major, as V's codes lie)
 //   warp 17          finds the CTA's units
+//   warp 19          looks for scales that lie too far apart
 //   warps 16, 18     issue S_t = Q_t K^T and O_t += P_t V of one tile each (tcgen05, f16 operands, fp32 sums)
 // so matrix products, exponentials and the widening of the next blocks' codes run side by side.  A block is worked on
 // in halves of 64 keys: in tensor memory stand S_0, S_1 (two halves of 64 columns each, the first 32 of a half
@@ -807,6 +808,14 @@ __global__ void __launch_bounds__(kFewThreads, few_resident(NT)) attend_few_kern
 // E2M1 times a power of two is exact in f16: K is held relative to the largest scale of a warp's 32 tokens (which
 // goes into those columns' score factor), V relative to a reference above the largest scale met in the unit (rescaled like
 // the softmax reference when it moves), with 2^12 on top, so scales down to 2^-26 of the largest are exact.
+//
+// That is not enough where V's scales lie further apart than 2^kManySpan: blocks vanish, and the weights are f16, too, off by
+// 2^-31 of the largest where they are small, which a value 2^16 larger than the largest weight's makes 2^-15 of that
+// one's share.  Warp 19 looks at the units' scales on its own, and when the CTA is through its units it does those again,
+// WIDE, with operands in bf16, whose exponents are fp32's: weights as the sum of two (2^-17 of themselves; the second over
+// the other half of the scores' columns) and V relative to wide_reference of each block of elements.  A unit takes 1.8 times
+// as long that way, 2.8 times in all (prompt of 8192 tokens, a value 2^40 times larger in each head: 0.64 / 1.8 ms).  A
+// branch in the roles' loops instead, or the look at the scales in the role that widens V, cost every call 15 % and more.
 //
 // Measured: a prompt of 8192 tokens, 32 heads of 128 on 8, 605 us, 910 TFLOP/s of the pairs the mask leaves (tensor
 // pipe half busy).  Neither the exponentials (replaced by a product: 583 us) nor the widening (left out: 577 us) bound
@@ -821,7 +830,9 @@ constexpr int kManyThreads = 640;
 constexpr int kManyLaunchRegs = 96, kSoftmaxRegs = 112, kCodeRegs = 96, kIssueRegs = 64;
 static_assert(2 * kSoftmaxRegs + 2 * kCodeRegs + kIssueRegs <= 5 * kManyLaunchRegs, "registers of a CTA");
 constexpr int kOperandLift = 12;
-constexpr int kManyUnits = 4;
+constexpr int kManyUnits = 4, kUnitReaders = 18;
+constexpr int kManySpan = 16;
+constexpr int kRedoUnits = 2048;     // units of a CTA that are told apart (of those behind, all are done again or none)
 
 template <int D>
 struct ManyShared {
@@ -837,9 +848,15 @@ struct ManyShared {
     // and V's reference; a slot is rewritten after the products of block j + 2, whose softmax follows that of j.  r_full: V's is there
     int k_ref[4][4], gone[4][4], v_ref[4];
     int v_top[4];
+    uint32_t v_refs[4];  // of units done again: V's references of each block of elements (bytes)
+    uint2 v_tops[4];
     int abort;
     uint32_t tmem;
     PlaceShared place;
+    Place start;  // the CTA's range
+    // units (by their number in the range) whose scales lie too far apart: written by one warp; `redo_all`: from that on
+    uint32_t redo[kRedoUnits / 32];
+    int redo_any, redo_all;
     // the CTA's units in order, written by one warp (so that no other spends registers on finding them) and read
     // by the 18 that work on them; past the last one stands an empty one
     Unit unit[kManyUnits];
@@ -876,11 +893,17 @@ __device__ __forceinline__ bool next_unit(ManyShared<D>& sm, int n, int lane) {
     return sm.unit[n % kManyUnits].end > 0;
 }
 
-// One warp: writes the units.
 template <int D>
-__device__ __forceinline__ void many_units(const AttendParams& p, ManyShared<D>& sm, const Place& place, int lane) {
-    Walk walk(p, place);
+__device__ __forceinline__ bool must_redo(const ManyShared<D>& sm, int n) {
+    return n < kRedoUnits ? sm.redo[n >> 5] >> (n & 31) & 1u : sm.redo_all != 0;
+}
+
+// One warp: writes the units (WIDE: those that are done again).
+template <int D, bool WIDE>
+__device__ __forceinline__ void many_units(const AttendParams& p, ManyShared<D>& sm, int lane) {
+    Walk walk(p, sm.start);
     bool more = true;
+    int number = 0;
     for (int n = 0; more; ++n) {
         const int at = n % kManyUnits;
         if (n >= kManyUnits && !warp_wait(&sm.unit_free[at], ((n / kManyUnits) & 1) ^ 1, &sm.abort)) {
@@ -888,16 +911,99 @@ __device__ __forceinline__ void many_units(const AttendParams& p, ManyShared<D>&
             break;
         }
         Unit u;
-        more = walk.next(p, kManyShift, u);
+        do
+            more = walk.next(p, kManyShift, u);
+        while (WIDE && more && !must_redo<D>(sm, number++));
         if (!more) u.end = 0;
         if (lane == 0) {
             sm.unit[at] = u;
             mbar_arrive(&sm.unit_full[at]);
         }
     }
-    if (lane == 0) p.cuts[blockIdx.x] = walk.cut;
+    if (lane == 0 && (!WIDE || walk.cut.parts == 0)) p.cuts[blockIdx.x] = walk.cut;
 }
 
+// One warp: looks at the scales of the units' V, and notes the units whose scales lie too far apart.  (It reads them
+// for itself: the roles that widen codes have no time for it.)  A first look, of 2 instructions a word: four scales plus
+// 136 - c, c one of the unit's own, are 128 .. 143, or off by a carry, if all of them lie within 2^8 of c (c far enough
+// from 0 and 255 that nothing wraps into that).  Where one does not, a second look takes the largest and the smallest but 0.
+template <int D>
+__device__ __forceinline__ void many_ranges(const AttendParams& p, ManyShared<D>& sm, int lane) {
+    constexpr int kBlocks = D / 32, kTokens = 16 / kBlocks;  // of a lane's 16 bytes of scales
+    const PageLayout<D> lay{p.page_size};
+    const uint32_t page_stride = static_cast<uint32_t>(p.Hk * lay.bytes());
+    for (int n = 0; next_unit<D>(sm, n, lane); ++n) {
+        const Unit& u = sm.unit[n % kManyUnits];
+        const int32_t* table = p.tables + u.t.b * p.table_width;
+        const int first = max(u.t.sp.first_lo, u.begin << kManyShift), last = min(u.t.sp.last_hi, (u.end << kManyShift) - 1);
+        const uint8_t* head = p.cache + u.kvh * lay.bytes() + lay.v_scales();
+        // the scales at token t, or null (an absent page is reported where it is used)
+        auto scales = [&](int t) -> const uint8_t* {
+            const int32_t pg = table[t >> p.page_shift];
+            if (static_cast<unsigned>(pg) >= static_cast<uint64_t>(p.num_pages)) return nullptr;
+            return head + static_cast<uint64_t>(static_cast<uint32_t>(pg)) * page_stride + (t & (p.page_size - 1)) * kBlocks;
+        };
+        // what of a lane's word i is seen
+        auto mask = [&](int t, int i) {  // D = 128: a token's four scales; D = 64: two tokens' two, in either half
+            const int t0 = t + i * kTokens / 4, t1 = t + (i * kTokens + kTokens / 2) / 4;
+            return (t0 >= first && t0 <= last ? 0x0000FFFFu : 0u) | (t1 >= first && t1 <= last ? 0xFFFF0000u : 0u);
+        };
+        const int from = (first & -kTokens) + kTokens * lane;
+        const uint8_t* one = first <= last ? scales(first) : nullptr;
+        const uint32_t vc = one ? __ldcg(one) : 0;
+        bool far = first <= last && vc - 16 > 223;
+        if (!far) {
+            const uint32_t vb = (136 - vc & 0xFFu) * 0x01010101u;
+            uint32_t out = 0;
+#pragma unroll 1
+            for (int t = from; t <= last; t += 32 * kTokens) {
+                const uint8_t* at = scales(t);
+                if (!at) continue;
+                uint4 v = __ldcg(reinterpret_cast<const uint4*>(at));
+                if (t < first || t + kTokens - 1 > last) {
+                    uint32_t* vw = reinterpret_cast<uint32_t*>(&v);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint32_t see = mask(t, i);
+                        vw[i] = (vw[i] & see) | (vc * 0x01010101u & ~see);
+                    }
+                }
+                out |= (v.x + vb ^ 0x80808080u) | (v.y + vb ^ 0x80808080u) | (v.z + vb ^ 0x80808080u) | (v.w + vb ^ 0x80808080u);
+            }
+            far = (out & 0xF0F0F0F0u) != 0;
+        }
+        if (!__any_sync(0xFFFFFFFFu, far)) continue;
+        // the largest, the smallest but 0 less 1, in either half
+        uint32_t vtop = 0, vlow = 0xFFFFFFFFu;
+#pragma unroll 1
+        for (int t = from; t <= last; t += 32 * kTokens) {
+            const uint8_t* at = scales(t);
+            if (!at) continue;
+#pragma unroll 1
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t see = mask(t, i);
+                const uint32_t v = __ldcg(reinterpret_cast<const uint32_t*>(at) + i) & see;
+                const uint32_t ve = v & 0x00FF00FFu, vo = v >> 8 & 0x00FF00FFu;
+                vtop = __vmaxu2(vtop, __vmaxu2(ve, vo));
+                vlow = __viaddmin_u16x2(vo, 0xFFFFFFFFu, __viaddmin_u16x2(ve, 0xFFFFFFFFu, vlow));
+            }
+        }
+        auto span = [](uint32_t top, uint32_t low) {  // negative where all are 0
+            return static_cast<int>(__reduce_max_sync(0xFFFFFFFFu, max(top & 0xFFFFu, top >> 16))) -
+                   static_cast<int>(__reduce_min_sync(0xFFFFFFFFu, min(low & 0xFFFFu, low >> 16))) - 1;
+        };
+        if (span(vtop, vlow) > kManySpan && lane == 0) {
+            sm.redo_any = 1;
+            if (n < kRedoUnits)
+                sm.redo[n >> 5] |= 1u << (n & 31);
+            else
+                sm.redo_all = 1;
+        }
+    }
+}
+
+// (of all warps, from wherever they are: their roles' code is not one place)
+__device__ __forceinline__ void cta_sync() { asm volatile("bar.sync 0;" ::: "memory"); }
 __device__ __forceinline__ void group_sync(int id) { asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory"); }
 
 // Codes of a warp's 32 tokens of K or V on their way through shared memory, one block ahead; the pages' numbers
@@ -991,9 +1097,19 @@ __device__ __forceinline__ uint4 widen_codes(uint32_t codes, uint32_t scale2) {
     }
     return make_uint4(h[0], h[1], h[2], h[3]);
 }
-// f16 2^(e - ref + kOperandLift) in both halves, 0 below the smallest normal (e <= ref).
+__device__ __forceinline__ uint4 widen_codes_bf16(uint32_t codes, uint32_t scale2) {
+    uint32_t h[4];
+    e2m1x8_to_f16(codes, h);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) h[i] = mul_bf16x2(e2m1_f16_to_bf16(h[i]), scale2);
+    return make_uint4(h[0], h[1], h[2], h[3]);
+}
+// f16 2^(e - ref + kOperandLift) in both halves, 0 below the smallest normal (e <= ref); bf16 2^(e - ref).
 __device__ __forceinline__ uint32_t operand_scale(uint32_t e, int ref) {
     return static_cast<uint32_t>(max(static_cast<int>(e) - ref + 15 + kOperandLift, 0)) * 0x04000400u;
+}
+__device__ __forceinline__ uint32_t operand_scale_bf16(uint32_t e, int ref) {
+    return static_cast<uint32_t>(max(static_cast<int>(e) - ref + 127, 0)) * 0x00800080u;
 }
 __device__ __forceinline__ int byte_max(uint32_t w) {
     return max(max(w & 0xFFu, (w >> 8) & 0xFFu), max((w >> 16) & 0xFFu, w >> 24));
@@ -1058,7 +1174,7 @@ __device__ __forceinline__ void many_keys(const AttendParams& p, ManyShared<D>& 
     cp_async_wait<0>();
 }
 
-template <int D>
+template <int D, bool WIDE>
 __device__ __forceinline__ void many_values(const AttendParams& p, ManyShared<D>& sm, int w, int lane) {
     constexpr int kBlocks = D / 32, kWords = kBlocks / 2;
     uint8_t* raw = sm.raw[4 + w];
@@ -1069,6 +1185,7 @@ __device__ __forceinline__ void many_values(const AttendParams& p, ManyShared<D>
     // by 2 chunks, whose 16-byte stores meet 8 different banks
     const int c = ((lane >> 2) & 1) + ((lane >> 3) & 1) * 2, pr = (lane & 3) + (lane >> 4) * 4;
     int ref = 0;
+    uint32_t refs = 0;  // WIDE: of each block of elements
     for (int j = 0; pending; ++j) {
         uint32_t code[2][4 * kWords], scale[2][2];
         cp_async_wait<0>();
@@ -1102,7 +1219,7 @@ __device__ __forceinline__ void many_values(const AttendParams& p, ManyShared<D>
                 top = max(top, byte_max(scale[i][r]));
             }
         }
-        if (cs.fresh) ref = 0;  // nothing of one unit's values reaches another's
+        if (cs.fresh) ref = 0, refs = 0;  // nothing of one unit's values reaches another's
         __syncwarp();
         pending = cs.more;
         cs.request(raw);
@@ -1117,6 +1234,35 @@ __device__ __forceinline__ void many_values(const AttendParams& p, ManyShared<D>
         group_sync(2);
         if (top == kNoBlock) break;
         if (top > ref) ref = min(top + 3, 254);  // room for three doublings before the next time
+        int unit[kBlocks];  // WIDE: wide_reference of each block of elements
+        if constexpr (WIDE) {
+            uint2 tops = make_uint2(0, 0);  // blocks 0 and 2, 1 and 3
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                tops.x = __vmaxu2(tops.x, scale[i >> 1][i & 1] & 0x00FF00FFu);
+                tops.y = __vmaxu2(tops.y, scale[i >> 1][i & 1] >> 8 & 0x00FF00FFu);
+            }
+            for (int x = 1; x < 32; x <<= 1) {
+                tops.x = __vmaxu2(tops.x, __shfl_xor_sync(0xFFFFFFFFu, tops.x, x));
+                tops.y = __vmaxu2(tops.y, __shfl_xor_sync(0xFFFFFFFFu, tops.y, x));
+            }
+            if (lane == 0) sm.v_tops[w] = tops;
+            group_sync(2);
+            for (int x = 0; x < 4; ++x) tops.x = __vmaxu2(tops.x, sm.v_tops[x].x), tops.y = __vmaxu2(tops.y, sm.v_tops[x].y);
+            group_sync(2);
+            const uint32_t old = refs;
+            uint32_t units = 0;
+            refs = 0;
+#pragma unroll
+            for (int b = 0; b < kBlocks; ++b) {
+                const uint32_t t = (b & 1 ? tops.y : tops.x) >> (16 * (b >> 1)) & 0xFFu, r = old >> (8 * b) & 0xFFu;
+                const uint32_t now = t > r ? min(t + 3, 254u) : r;
+                refs |= now << (8 * b);
+                unit[b] = wide_reference(static_cast<int>(now));
+                units |= static_cast<uint32_t>(unit[b]) << (8 * b);
+            }
+            if (lane == 0 && w == 0) sm.v_refs[j & 3] = units;
+        }
         if (lane == 0 && w == 0) {
             sm.v_ref[j & 3] = ref;
             mbar_arrive(&sm.r_full[j & 3]);
@@ -1131,9 +1277,10 @@ __device__ __forceinline__ void many_values(const AttendParams& p, ManyShared<D>
                     // four codes of elements 8c .. and four of 8c + 4 ..
                     const uint32_t x = code[i][r * kWords + (b >> 1)], y = code[i][(2 + r) * kWords + (b >> 1)];
                     const uint32_t word = __byte_perm(x, y, b & 1 ? 0x7632 : 0x5410);
-                    const uint32_t s2 = operand_scale((scale[i][r] >> (8 * b)) & 0xFFu, ref);
+                    const uint32_t e = (scale[i][r] >> (8 * b)) & 0xFFu;
                     const int chunk = (4 * (b & 1) + c) ^ (row & 7);
-                    *reinterpret_cast<uint4*>(sm.v[stage] + (b >> 1) * 16384 + row * 128 + chunk * 16) = widen_codes(word, s2);
+                    *reinterpret_cast<uint4*>(sm.v[stage] + (b >> 1) * 16384 + row * 128 + chunk * 16) =
+                        WIDE ? widen_codes_bf16(word, operand_scale_bf16(e, unit[b])) : widen_codes(word, operand_scale(e, ref));
                 }
             }
         }
@@ -1144,11 +1291,12 @@ __device__ __forceinline__ void many_values(const AttendParams& p, ManyShared<D>
 }
 
 // One warp: the matrix products of tile t, issued by one of its lanes.
-template <int D>
+template <int D, bool WIDE>
 __device__ __forceinline__ void many_products(ManyShared<D>& sm, int t, int lane) {
     constexpr uint32_t kF32 = 1u << 4;  // fp32 sums, f16 operands
     constexpr uint32_t kScoreDesc = kF32 | ((64u >> 3) << 17) | ((128u >> 4) << 24);
-    constexpr uint32_t kValueDesc = kF32 | (1u << 16) | (static_cast<uint32_t>(D >> 3) << 17) | ((128u >> 4) << 24);
+    constexpr uint32_t kBf16 = 1u << 7 | 1u << 10;
+    constexpr uint32_t kValueDesc = kF32 | (WIDE ? kBf16 : 0u) | (1u << 16) | (static_cast<uint32_t>(D >> 3) << 17) | ((128u >> 4) << 24);
     constexpr uint32_t kNext = ManyShared<D>::kTile >> 4, kHalf = 64 * 128 >> 4;
     const uint32_t tm = sm.tmem + 128 * t;
     const uint64_t qd = desc_sw128(smem_u32(sm.q[t])), k0 = desc_sw128(smem_u32(sm.k[0]));
@@ -1187,6 +1335,11 @@ __device__ __forceinline__ void many_products(ManyShared<D>& sm, int t, int lane
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
                         tc_mma_f16_ts(tm + 256, tm + 64 * half + 8 * k, vd + (k * 2048 >> 4), kValueDesc, h == 1 && k == 0 ? 0u : 1u);
+                    if constexpr (WIDE) {  // what bf16 left of the weights
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            tc_mma_f16_ts(tm + 256, tm + 64 * half + 32 + 8 * k, vd + (k * 2048 >> 4), kValueDesc, 1u);
+                    }
                     tc_commit(&sm.o_done[t]);
                     if (h == halves) tc_commit(&sm.o_full[t]);
                     if (half == 1) tc_commit(&sm.v_free[b & 1]);
@@ -1257,13 +1410,14 @@ __device__ __forceinline__ QueryRow load_query(const AttendParams& p, ManyShared
     return q;
 }
 
-template <int D>
+template <int D, bool WIDE>
 __device__ __forceinline__ void many_softmax(const AttendParams& p, ManyShared<D>& sm, int t, int tid) {
     const uint32_t lanes = static_cast<uint32_t>(tid & 96) << 16;  // the warp's 32 lanes of tensor memory
     const uint32_t ts = sm.tmem + 128 * t + lanes, to = sm.tmem + 256 + 128 * t + lanes;
     int j = 0, units = 0;
     float ref = 0.0f, bound = -INFINITY, sum = 0.0f;
     int vref = 0;
+    uint32_t vunit = 0;  // WIDE: what the sums of each block of elements count units of
     int64_t slot = -1;
     QueryRow row = {0, -1, -1, 1.0f};
     for (;; ++units) {
@@ -1279,7 +1433,7 @@ __device__ __forceinline__ void many_softmax(const AttendParams& p, ManyShared<D
             if (!warp_wait(&sm.o_full[t], (units - 1) & 1, &sm.abort)) return;
             tc_fence_after();
             const float inv = sum > 0.0f ? 1.0f / sum : sum == 0.0f ? 0.0f : sum;
-            const float vs = vref > kOperandLift ? __uint_as_float(static_cast<uint32_t>(vref - kOperandLift) << 23) : 0.0f;
+            float vs = vref > kOperandLift ? __uint_as_float(static_cast<uint32_t>(vref - kOperandLift) << 23) : 0.0f;
             const float m = bound == -INFINITY && sum == 0.0f ? -INFINITY : ref;  // (a row that is not finite: NaN)
             const int64_t at = out_slot * kManyRows + 128 * t + tid;
 #pragma unroll 1
@@ -1287,6 +1441,7 @@ __device__ __forceinline__ void many_softmax(const AttendParams& p, ManyShared<D
                 float2 o[16];
                 tmem_ld32(to + 32 * b, *reinterpret_cast<uint32_t(*)[32]>(o));
                 tmem_ld_wait();
+                if constexpr (WIDE) vs = __uint_as_float((vunit >> (8 * b) & 0xFFu) << 23);
                 const float2 i2 = make_float2(inv, inv), v2 = make_float2(vs, vs);
 #pragma unroll
                 for (int i = 0; i < 16; ++i) o[i] = __fmul2_rn(__fmul2_rn(o[i], i2), v2);
@@ -1316,7 +1471,7 @@ __device__ __forceinline__ void many_softmax(const AttendParams& p, ManyShared<D
             }
         }
         if (!more) return;
-        ref = 0.0f, bound = -INFINITY, sum = 0.0f, vref = 0;
+        ref = 0.0f, bound = -INFINITY, sum = 0.0f, vref = 0, vunit = 0;
         const int begin = unit.begin, halves = 2 * (unit.end - unit.begin);
 #pragma unroll 1
         for (int h = 0; h < halves; ++h) {  // 64 keys
@@ -1369,8 +1524,9 @@ __device__ __forceinline__ void many_softmax(const AttendParams& p, ManyShared<D
                 m = fmaxf(m, fmaxf(a, z) * f[i]);
             }
             const int nv = sm.v_ref[b & 3];
-            if (__any_sync(0xFFFFFFFFu, m > bound || nv != vref)) {
-                float scale = nv - vref < 127 ? __uint_as_float(static_cast<uint32_t>(127 - (nv - vref)) << 23) : 0.0f;
+            const uint32_t nunit = WIDE ? sm.v_refs[b & 3] : 0;
+            if (__any_sync(0xFFFFFFFFu, m > bound || nv != vref || nunit != vunit)) {
+                float scale = WIDE ? 1.0f : nv - vref < 127 ? __uint_as_float(static_cast<uint32_t>(127 - (nv - vref)) << 23) : 0.0f;
                 vref = nv;
                 if (m > bound - kSlack) {  // false while the row has seen nothing
                     const float old = ref;
@@ -1388,26 +1544,39 @@ __device__ __forceinline__ void many_softmax(const AttendParams& p, ManyShared<D
                         uint32_t o[16];
                         tmem_ld16(to + 16 * i, o);
                         tmem_ld_wait();
+                        float more = 1.0f, by = scale;
+                        if constexpr (WIDE) {  // and by 2^(old unit - new unit), in two factors that are normal numbers
+                            const int d = static_cast<int>(nunit >> (4 * i & 24) & 0xFFu) - static_cast<int>(vunit >> (4 * i & 24) & 0xFFu);
+                            by *= __uint_as_float(static_cast<uint32_t>(127 - d / 2) << 23);
+                            more = __uint_as_float(static_cast<uint32_t>(127 - (d - d / 2)) << 23);
+                        }
 #pragma unroll
-                        for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * scale);
+                        for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * by * more);
                         tmem_st16(to + 16 * i, o);
                     }
                 }
+                vunit = nunit;
             }
             float2 add[2] = {};
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const float2 f2 = make_float2(f[i], f[i]), r2 = make_float2(-ref, -ref);
-                uint32_t w[16];
+                uint32_t w[16], rest[16];
 #pragma unroll
                 for (int k = 0; k < 16; ++k) {
                     float2 e = __ffma2_rn(make_float2(s[32 * i + 2 * k], s[32 * i + 2 * k + 1]), f2, r2);
                     e = make_float2(exp2_approx(e.x), exp2_approx(e.y));
                     add[k & 1] = __fadd2_rn(add[k & 1], e);
+                    if constexpr (WIDE) {
+                        w[k] = pack_bf16(e.x, e.y);
+                        rest[k] = pack_bf16(e.x - bf_lo(w[k]), e.y - bf_hi(w[k]));
+                        continue;
+                    }
                     const __half2 y = __floats2half2_rn(e.x, e.y);
                     w[k] = *reinterpret_cast<const uint32_t*>(&y);
                 }
                 tmem_st16(th + 16 * i, w);  // over scores that have been read
+                if constexpr (WIDE) tmem_st16(th + 32 + 16 * i, rest);
             }
             sum += (add[0].x + add[0].y) + (add[1].x + add[1].y);
             tmem_st_wait();
@@ -1418,6 +1587,54 @@ __device__ __forceinline__ void many_softmax(const AttendParams& p, ManyShared<D
     }
 }
 
+// One thread: all barriers as new (`again`: nothing arrives at the old ones any more).
+template <int D>
+__device__ __forceinline__ void many_init(ManyShared<D>& sm, bool again, uint32_t unit_readers) {
+    auto init = [again](uint64_t* bar, uint32_t count) {
+        if (again) mbar_inval(bar);
+        mbar_init(bar, count);
+    };
+    for (int i = 0; i < 2; ++i) {
+        init(&sm.k_full[i], 4), init(&sm.k_free[i], 2);
+        init(&sm.v_full[i], 4), init(&sm.v_free[i], 2);
+        init(&sm.q_full[i], 4), init(&sm.o_done[i], 1), init(&sm.o_full[i], 1);
+        for (int h = 0; h < 2; ++h) init(&sm.s_full[i][h], 2), init(&sm.p_full[i][h], 4);
+    }
+    for (int i = 0; i < 4; ++i) init(&sm.r_full[i], 1);
+    init(&sm.drained[0], 1), init(&sm.drained[1], 1);
+    for (int i = 0; i < kManyUnits; ++i) init(&sm.unit_full[i], 1), init(&sm.unit_free[i], unit_readers);
+    fence_mbar_init();
+}
+
+// All threads, each in its role, when the CTA's units are done: whether some are to be done again, with barriers as new.
+template <int D>
+__device__ __forceinline__ bool many_again(ManyShared<D>& sm) {
+    tc_fence_before();
+    cta_sync();
+    if (!sm.redo_any || sm.abort) return false;
+    if (threadIdx.x == 0) many_init(sm, true, kUnitReaders);
+    cta_sync();
+    tc_fence_after();
+    return true;
+}
+
+template <int D, bool WIDE>
+__device__ __forceinline__ void many_issue(const AttendParams& p, ManyShared<D>& sm, int warp, int lane) {
+    if (warp == 17) many_units<D, WIDE>(p, sm, lane);
+    if (!WIDE && warp == 19) many_ranges<D>(p, sm, lane);
+    if (warp == 16 || warp == 18) {
+        const int t = (warp - 16) >> 1;
+        many_products<D, WIDE>(sm, t, lane);
+        __syncwarp();
+        if (elect_one()) {
+            int gave_up = 0;  // nothing is in flight when tensor memory is given back, whatever happened
+            tc_commit(&sm.drained[t]);
+            mbar_wait(&sm.drained[t], 0, &gave_up);
+        }
+    }
+    __syncwarp();
+}
+
 template <int D>
 __global__ void __launch_bounds__(kManyThreads, 1) attend_many_kernel(const __grid_constant__ AttendParams p) {
     extern __shared__ __align__(1024) uint8_t dynamic_many[];
@@ -1425,51 +1642,39 @@ __global__ void __launch_bounds__(kManyThreads, 1) attend_many_kernel(const __gr
         dynamic_many + ((1024 - (smem_u32(dynamic_many) & 1023)) & 1023));
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     if (threadIdx.x == 0) {
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&sm.k_full[i], 4), mbar_init(&sm.k_free[i], 2);
-            mbar_init(&sm.v_full[i], 4), mbar_init(&sm.v_free[i], 2);
-            mbar_init(&sm.q_full[i], 4), mbar_init(&sm.o_done[i], 1), mbar_init(&sm.o_full[i], 1);
-            for (int h = 0; h < 2; ++h) mbar_init(&sm.s_full[i][h], 2), mbar_init(&sm.p_full[i][h], 4);
-        }
-        for (int i = 0; i < 4; ++i) mbar_init(&sm.r_full[i], 1);
-        mbar_init(&sm.drained[0], 1), mbar_init(&sm.drained[1], 1);
-        for (int i = 0; i < kManyUnits; ++i) mbar_init(&sm.unit_full[i], 1), mbar_init(&sm.unit_free[i], 18);
-        sm.abort = 0;
-        fence_mbar_init();
+        many_init(sm, false, kUnitReaders + 1);  // and the warp that looks at the scales
+        sm.abort = 0, sm.redo_any = 0, sm.redo_all = 0;
     }
+    if (threadIdx.x < kRedoUnits / 32) sm.redo[threadIdx.x] = 0;
     if (warp == 16) {
         tmem_alloc(&sm.tmem, 512);
         tmem_relinquish();
     }
     griddep_launch_dependents();
     griddep_wait();
-    const Place place = find_place<kManyThreads>(p, kManyShift, blockIdx.x, sm.place);
+    {
+        const Place place = find_place<kManyThreads>(p, kManyShift, blockIdx.x, sm.place);
+        if (threadIdx.x == 0) sm.start = place;
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     if (warp < 8) {
         setmaxnreg_inc<kSoftmaxRegs>();
-        many_softmax<D>(p, sm, warp >> 2, threadIdx.x & 127);
+        many_softmax<D, false>(p, sm, warp >> 2, threadIdx.x & 127);
+        if (many_again(sm)) many_softmax<D, true>(p, sm, warp >> 2, threadIdx.x & 127);
     } else if (warp < 12) {
         setmaxnreg_dec<kCodeRegs>();
         many_keys<D>(p, sm, warp - 8, lane);
+        if (many_again(sm)) many_keys<D>(p, sm, warp - 8, lane);
     } else if (warp < 16) {
         setmaxnreg_dec<kCodeRegs>();
-        many_values<D>(p, sm, warp - 12, lane);
+        many_values<D, false>(p, sm, warp - 12, lane);
+        if (many_again(sm)) many_values<D, true>(p, sm, warp - 12, lane);
     } else {
         setmaxnreg_dec<kIssueRegs>();
-        if (warp == 17) many_units<D>(p, sm, place, lane);
-        if (warp == 16 || warp == 18) {
-            const int t = (warp - 16) >> 1;
-            many_products<D>(sm, t, lane);
-            __syncwarp();
-            if (elect_one()) {
-                int gave_up = 0;  // nothing is in flight when tensor memory is given back, whatever happened
-                tc_commit(&sm.drained[t]);
-                mbar_wait(&sm.drained[t], 0, &gave_up);
-            }
-        }
-        __syncwarp();
+        many_issue<D, false>(p, sm, warp, lane);
+        if (many_again(sm)) many_issue<D, true>(p, sm, warp, lane);
     }
     tc_fence_before();
     __syncthreads();
