@@ -434,7 +434,9 @@ int macaq_kv4_gather(const uint8_t* cache, int64_t num_pages, int page_size, int
  * weights.  Values may lie as far apart as they like, seen by a row or not: where a unit of work (a kv head of a
  * sequence and a tile of its query rows) meets V scales more than 2^11 to 2^16 apart, it is done again with weights as
  * sums of two bf16, which takes 2 to 3 times as long; values then count down to 2^-196 of the largest of the same
- * 32 elements.  An infinity or NaN is stored as values of some 2^126: rows that may not see it are not changed by it.
+ * 32 elements.  Keys likewise; in the kernel of many query rows, blocks of a key below 2^-26 (2^-10 beside keys 2^16 times as
+ * large) of its own largest block count as zero.  An infinity or NaN is stored as values of some 2^126: rows that may not
+ * see it are not changed by it, one that sees such a key may be NaN.
  */
 size_t macaq_kv4_attention_workspace_bytes(int64_t T, int64_t B, int Hq, int Hk, int head_dim, int64_t max_q);
 int macaq_kv4_attention(const uint16_t* q, int64_t T, int64_t ldq, int Hq, int Hk, int head_dim,

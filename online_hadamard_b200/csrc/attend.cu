@@ -811,9 +811,11 @@ __global__ void __launch_bounds__(kFewThreads, few_resident(NT)) attend_few_kern
 //
 // That is not enough where V's scales lie further apart than 2^kManySpan: blocks vanish, and the weights are f16, too, off by
 // 2^-31 of the largest where they are small, which a value 2^16 larger than the largest weight's makes 2^-15 of that
-// one's share.  Warp 19 looks at the units' scales on its own, and when the CTA is through its units it does those again,
+// one's share.  Where K's scales lie as far apart, a token can be lost beside another of the 32 that a row may not see
+// or gives no weight.  Warp 19 looks at the units' scales on its own, and when the CTA is through its units it does those again,
 // WIDE, with operands in bf16, whose exponents are fp32's: weights as the sum of two (2^-17 of themselves; the second over
-// the other half of the scores' columns) and V relative to wide_reference of each block of elements.  A unit takes 1.8 times
+// the other half of the scores' columns), V relative to wide_reference of each block of elements, and K's tokens relative to
+// their own largest scales, which then go into each column's score.  A unit takes 1.8 times
 // as long that way, 2.8 times in all (prompt of 8192 tokens, a value 2^40 times larger in each head: 0.64 / 1.8 ms).  A
 // branch in the roles' loops instead, or the look at the scales in the role that widens V, cost every call 15 % and more.
 //
@@ -833,6 +835,8 @@ constexpr int kOperandLift = 12;
 constexpr int kManyUnits = 4, kUnitReaders = 18;
 constexpr int kManySpan = 16;
 constexpr int kRedoUnits = 2048;     // units of a CTA that are told apart (of those behind, all are done again or none)
+// WIDE, a column's factor is 2^(its token's largest scale - kKeyReference): 2^60 for an infinity's, where products reach 2^38
+constexpr int kKeyReference = 193;
 
 template <int D>
 struct ManyShared {
@@ -848,7 +852,9 @@ struct ManyShared {
     // and V's reference; a slot is rewritten after the products of block j + 2, whose softmax follows that of j.  r_full: V's is there
     int k_ref[4][4], gone[4][4], v_ref[4];
     int v_top[4];
-    uint32_t v_refs[4];  // of units done again: V's references of each block of elements (bytes)
+    // of units done again: what each key's scores are multiplied by, V's references of each block of elements (bytes)
+    alignas(16) float k_factor[4][128];
+    uint32_t v_refs[4];
     uint2 v_tops[4];
     int abort;
     uint32_t tmem;
@@ -923,7 +929,7 @@ __device__ __forceinline__ void many_units(const AttendParams& p, ManyShared<D>&
     if (lane == 0 && (!WIDE || walk.cut.parts == 0)) p.cuts[blockIdx.x] = walk.cut;
 }
 
-// One warp: looks at the scales of the units' V, and notes the units whose scales lie too far apart.  (It reads them
+// One warp: looks at the scales of the units' K and V, and notes the units whose scales lie too far apart.  (It reads them
 // for itself: the roles that widen codes have no time for it.)  A first look, of 2 instructions a word: four scales plus
 // 136 - c, c one of the unit's own, are 128 .. 143, or off by a carry, if all of them lie within 2^8 of c (c far enough
 // from 0 and 255 that nothing wraps into that).  Where one does not, a second look takes the largest and the smallest but 0.
@@ -936,8 +942,9 @@ __device__ __forceinline__ void many_ranges(const AttendParams& p, ManyShared<D>
         const Unit& u = sm.unit[n % kManyUnits];
         const int32_t* table = p.tables + u.t.b * p.table_width;
         const int first = max(u.t.sp.first_lo, u.begin << kManyShift), last = min(u.t.sp.last_hi, (u.end << kManyShift) - 1);
-        const uint8_t* head = p.cache + u.kvh * lay.bytes() + lay.v_scales();
-        // the scales at token t, or null (an absent page is reported where it is used)
+        const uint8_t* head = p.cache + u.kvh * lay.bytes() + lay.k_scales();
+        const int v_at = p.page_size * kBlocks;
+        // the scales of K at token t (those of V are v_at further), or null (an absent page is reported where it is used)
         auto scales = [&](int t) -> const uint8_t* {
             const int32_t pg = table[t >> p.page_shift];
             if (static_cast<unsigned>(pg) >= static_cast<uint64_t>(p.num_pages)) return nullptr;
@@ -950,31 +957,34 @@ __device__ __forceinline__ void many_ranges(const AttendParams& p, ManyShared<D>
         };
         const int from = (first & -kTokens) + kTokens * lane;
         const uint8_t* one = first <= last ? scales(first) : nullptr;
-        const uint32_t vc = one ? __ldcg(one) : 0;
-        bool far = first <= last && vc - 16 > 223;
+        const uint32_t kc = one ? __ldcg(one) : 0, vc = one ? __ldcg(one + v_at) : 0;
+        bool far = first <= last && (kc - 16 > 223 || vc - 16 > 223);
         if (!far) {
-            const uint32_t vb = (136 - vc & 0xFFu) * 0x01010101u;
+            const uint32_t kb = (136 - kc & 0xFFu) * 0x01010101u, vb = (136 - vc & 0xFFu) * 0x01010101u;
             uint32_t out = 0;
 #pragma unroll 1
             for (int t = from; t <= last; t += 32 * kTokens) {
                 const uint8_t* at = scales(t);
                 if (!at) continue;
-                uint4 v = __ldcg(reinterpret_cast<const uint4*>(at));
+                uint4 k = __ldcg(reinterpret_cast<const uint4*>(at)), v = __ldcg(reinterpret_cast<const uint4*>(at + v_at));
                 if (t < first || t + kTokens - 1 > last) {
+                    uint32_t* kw = reinterpret_cast<uint32_t*>(&k);
                     uint32_t* vw = reinterpret_cast<uint32_t*>(&v);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const uint32_t see = mask(t, i);
+                        kw[i] = (kw[i] & see) | (kc * 0x01010101u & ~see);
                         vw[i] = (vw[i] & see) | (vc * 0x01010101u & ~see);
                     }
                 }
-                out |= (v.x + vb ^ 0x80808080u) | (v.y + vb ^ 0x80808080u) | (v.z + vb ^ 0x80808080u) | (v.w + vb ^ 0x80808080u);
+                out |= (k.x + kb ^ 0x80808080u) | (k.y + kb ^ 0x80808080u) | (k.z + kb ^ 0x80808080u) | (k.w + kb ^ 0x80808080u) |
+                       (v.x + vb ^ 0x80808080u) | (v.y + vb ^ 0x80808080u) | (v.z + vb ^ 0x80808080u) | (v.w + vb ^ 0x80808080u);
             }
             far = (out & 0xF0F0F0F0u) != 0;
         }
         if (!__any_sync(0xFFFFFFFFu, far)) continue;
-        // the largest, the smallest but 0 less 1, in either half
-        uint32_t vtop = 0, vlow = 0xFFFFFFFFu;
+        // of V's blocks, of K's tokens (each token's largest): the largest, the smallest but 0 less 1, in either half
+        uint32_t vtop = 0, vlow = 0xFFFFFFFFu, ktop = 0, klow = 0xFFFFFFFFu;
 #pragma unroll 1
         for (int t = from; t <= last; t += 32 * kTokens) {
             const uint8_t* at = scales(t);
@@ -982,17 +992,22 @@ __device__ __forceinline__ void many_ranges(const AttendParams& p, ManyShared<D>
 #pragma unroll 1
             for (int i = 0; i < 4; ++i) {
                 const uint32_t see = mask(t, i);
-                const uint32_t v = __ldcg(reinterpret_cast<const uint32_t*>(at) + i) & see;
+                const uint32_t k = __ldcg(reinterpret_cast<const uint32_t*>(at) + i) & see;
+                const uint32_t v = __ldcg(reinterpret_cast<const uint32_t*>(at + v_at) + i) & see;
                 const uint32_t ve = v & 0x00FF00FFu, vo = v >> 8 & 0x00FF00FFu;
                 vtop = __vmaxu2(vtop, __vmaxu2(ve, vo));
                 vlow = __viaddmin_u16x2(vo, 0xFFFFFFFFu, __viaddmin_u16x2(ve, 0xFFFFFFFFu, vlow));
+                uint32_t km = __vmaxu2(k & 0x00FF00FFu, k >> 8 & 0x00FF00FFu);
+                if (D == 128) km = __vmaxu2(km, __byte_perm(km, km, 0x1032));
+                ktop = __vmaxu2(ktop, km);
+                klow = __viaddmin_u16x2(km, 0xFFFFFFFFu, klow);
             }
         }
         auto span = [](uint32_t top, uint32_t low) {  // negative where all are 0
             return static_cast<int>(__reduce_max_sync(0xFFFFFFFFu, max(top & 0xFFFFu, top >> 16))) -
                    static_cast<int>(__reduce_min_sync(0xFFFFFFFFu, min(low & 0xFFFFu, low >> 16))) - 1;
         };
-        if (span(vtop, vlow) > kManySpan && lane == 0) {
+        if (max(span(vtop, vlow), span(ktop, klow)) > kManySpan && lane == 0) {
             sm.redo_any = 1;
             if (n < kRedoUnits)
                 sm.redo[n >> 5] |= 1u << (n & 31);
@@ -1115,7 +1130,7 @@ __device__ __forceinline__ int byte_max(uint32_t w) {
     return max(max(w & 0xFFu, (w >> 8) & 0xFFu), max((w >> 16) & 0xFFu, w >> 24));
 }
 
-template <int D>
+template <int D, bool WIDE>
 __device__ __forceinline__ void many_keys(const AttendParams& p, ManyShared<D>& sm, int w, int lane) {
     constexpr int kBlocks = D / 32;
     uint8_t* raw = sm.raw[w];
@@ -1148,19 +1163,23 @@ __device__ __forceinline__ void many_keys(const AttendParams& p, ManyShared<D>& 
 #pragma unroll
                 for (int b = 0; b < kBlocks; ++b) code[i][b] = 0;
             }
-            top = max(top, byte_max(scale[i]));
+            if constexpr (!WIDE) top = max(top, byte_max(scale[i]));
         }
         const uint32_t gone = cs.seen & ~cs.there;
         __syncwarp();
         pending = cs.more;
         cs.request(raw);
-        const int ref = static_cast<int>(__reduce_max_sync(0xFFFFFFFFu, static_cast<unsigned>(top)));
+        int ref = WIDE ? kKeyReference : static_cast<int>(__reduce_max_sync(0xFFFFFFFFu, static_cast<unsigned>(top)));
         const int stage = j & 1;
         if (j >= 2 && !warp_wait(&sm.k_free[stage], ((j >> 1) & 1) ^ 1, &sm.abort)) break;
         if (lane == 0) sm.k_ref[j & 3][w] = ref, sm.gone[j & 3][w] = static_cast<int>(gone);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int row = 32 * w + 8 * i + tok;
+            if constexpr (WIDE) {  // relative to the token's own largest scale
+                ref = byte_max(scale[i]);
+                if (c == 0) sm.k_factor[j & 3][row] = __uint_as_float(static_cast<uint32_t>(max(ref + 127 - kKeyReference, 1)) << 23);
+            }
 #pragma unroll
             for (int b = 0; b < kBlocks; ++b) {
                 const uint32_t s2 = operand_scale((scale[i] >> (8 * b)) & 0xFFu, ref);
@@ -1511,6 +1530,10 @@ __device__ __forceinline__ void many_softmax(const AttendParams& p, ManyShared<D
             tmem_ld32(th, *reinterpret_cast<uint32_t(*)[32]>(s));
             tmem_ld32(th + 32, *reinterpret_cast<uint32_t(*)[32]>(s + 32));
             tmem_ld_wait();
+            if constexpr (WIDE) {
+#pragma unroll
+                for (int k = 0; k < 64; ++k) s[k] *= sm.k_factor[b & 3][64 * half + k];
+            }
             float m = -INFINITY;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
@@ -1665,8 +1688,8 @@ __global__ void __launch_bounds__(kManyThreads, 1) attend_many_kernel(const __gr
         if (many_again(sm)) many_softmax<D, true>(p, sm, warp >> 2, threadIdx.x & 127);
     } else if (warp < 12) {
         setmaxnreg_dec<kCodeRegs>();
-        many_keys<D>(p, sm, warp - 8, lane);
-        if (many_again(sm)) many_keys<D>(p, sm, warp - 8, lane);
+        many_keys<D, false>(p, sm, warp - 8, lane);
+        if (many_again(sm)) many_keys<D, true>(p, sm, warp - 8, lane);
     } else if (warp < 16) {
         setmaxnreg_dec<kCodeRegs>();
         many_values<D, false>(p, sm, warp - 12, lane);

@@ -166,3 +166,32 @@ def test_other_sequences_keep_their_bits(mq, nq, Hk, gain):
     for b in bad:
         same[b * nq:(b + 1) * nq] = False
     assert torch.equal(out[same], want[same]) and torch.equal(lse[same], wl[same])
+
+
+@pytest.mark.parametrize("D,G,nq,Hk,page,room", KERNELS)
+@pytest.mark.parametrize("gain", [2.0 ** 20, 2.0 ** 40, np.inf, np.nan])
+def test_a_huge_key_that_earlier_queries_do_not_see(mq, D, G, nq, Hk, page, room, gain):
+    rng = np.random.default_rng(55)
+    k, v, q = sequence(rng, nq + 33, nq, G * Hk, Hk, D)
+    k *= 2.0
+    k[-1, :, 7] *= np.float32(gain)
+    Cached([(k, v, q)], page, room).check(mq, earlier)
+
+
+@pytest.mark.parametrize("D,G,nq,Hk,page,room", KERNELS)
+def test_a_huge_key_of_no_weight(mq, D, G, nq, Hk, page, room):
+    """A key of 2^30 times the others' size against the queries' direction: its neighbours' scores count all the same."""
+    rng = np.random.default_rng(56)
+    L = nq + 60
+    k, v, q = sequence(rng, L, nq, G * Hk, Hk, D, {j: 3.0 * np.sin(j) for j in range(L)})
+    k[17] = -np.abs(k[17]).max() * 2.0 ** 30 * np.sign(q[0, 0])
+    Cached([(kv.bf16(k), v, q)], page, room).check(mq)
+
+
+@pytest.mark.parametrize("nq", [1, 50])
+def test_keys_that_grow_along_the_sequence(mq, nq):
+    """Keys of 2^-40 to 2^4 among neighbours of the same 32 tokens."""
+    rng = np.random.default_rng(57)
+    k, v, q = sequence(rng, nq + 150, nq, 4, 2, 128)
+    k *= np.where(np.arange(len(k)) % 5 == 0, 2.0 ** -40, np.where(np.arange(len(k)) % 7 == 0, 2.0 ** 4, 1.0))[:, None, None]
+    Cached([(kv.bf16(k), v, q)], 32).check(mq)
