@@ -398,8 +398,8 @@ __device__ __forceinline__ void run_cache_blocks(const HeadParams& p, int64_t bl
 
 template <int D, RopeMode MODE, bool CACHE>
 __global__ void __launch_bounds__(kHeadThreads, 8) heads_kernel(const __grid_constant__ HeadParams p) {
-    griddep_launch_dependents();
     griddep_wait();  // the rows may be written, and the outputs read, by the preceding kernel
+    griddep_launch_dependents();  // (behind the wait: attend.cu says why)
     if constexpr (CACHE) {
         if (blockIdx.x < p.cache_blocks) {
             run_cache_blocks<D>(p, blockIdx.x, MODE == RopeMode::kPair);
@@ -426,8 +426,8 @@ __global__ void __launch_bounds__(kHeadThreads) kv4_gather_kernel(const uint8_t*
                                                                   int page_size, int Hk, const int64_t* slots,
                                                                   int64_t T, uint16_t* k, uint16_t* v) {
     constexpr int kBlocks = D / 32;
-    griddep_launch_dependents();
     griddep_wait();
+    griddep_launch_dependents();
     const int64_t item = static_cast<int64_t>(blockIdx.x) * kHeadThreads + threadIdx.x;
     const int b = static_cast<int>(item % kBlocks);
     int64_t rest = item / kBlocks;

@@ -195,3 +195,42 @@ def test_captured_prompt_follows_its_inputs(mq):
         assert torch.equal(out, want)
         assert (out[cu_now[-1]:] == 7).all()
     assert mq.macaq_device_status() == 0
+
+
+@pytest.mark.parametrize("nq", [1, 3, 40])
+def test_kernels_that_follow_one_another_share_their_buffers(mq, nq):
+    """append and attention of several batches in turn, nothing else between them, into the same queries and through
+    the same workspace: what one call leaves there (queries, parts, notes of cut units) is not taken for another's."""
+    rng = np.random.default_rng(41)
+    Hq, Hk, D, page, calls = 8, 1, 128, 32, []
+    q = torch.empty(2 * nq, Hq, D, dtype=torch.bfloat16, device="cuda")
+    ws = torch.empty(mq.kv4_attention_workspace_bytes(2 * nq, 2, Hq, Hk, D, nq), dtype=torch.uint8, device="cuda")
+    cu = cuda(np.array([0, nq, 2 * nq], np.int32))
+    for lens in ((1500, 70), (90, 1400), (1200, 1200), (64, 100), (40, 1990)):
+        p = Problem([(n, nq) for n in lens], Hq, Hk, D, page, seed=42 + lens[0], extra_rows=0)
+        x = kv.bf16(rng.standard_normal((2 * nq, (Hq + 2 * Hk) * D)))
+        at = np.concatenate([np.arange(n - nq, n) for n in lens])
+        slots = p.tables[np.repeat([0, 1], nq), at // page].astype(np.int64) * page + at % page
+        calls.append((cuda(x, torch.bfloat16), cuda(p.cache), cuda(slots), cuda(p.tables), cuda(p.kv_lens)))
+
+    def call(x, cache, slots, tables, lens, out=None):
+        mq.macaq_kv4_append(x, Hq, Hk, D, cache, page, slots, q=q)
+        return mq.macaq_kv4_attention(q, cache, page, tables, lens, cu, max_q=nq, out=out, workspace=ws)
+
+    want = []
+    for c in calls:
+        want.append(call(*c))
+        torch.cuda.synchronize()
+    order = rng.integers(0, len(calls), 60)
+    outs = [torch.empty_like(want[0]) for _ in order]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for i, out in zip(order, outs):
+            call(*calls[i], out=out)
+    for out in outs:
+        out.zero_()
+    graph.replay()
+    assert all(torch.equal(out, want[i]) for i, out in zip(order, outs))
+    got = [call(*calls[i]) for i in order]
+    assert all(torch.equal(out, want[i]) for i, out in zip(order, got))
+    assert mq.macaq_device_status() == 0
