@@ -1,7 +1,7 @@
 """Python binding of libmacaq: the MACaQ MXFP4 W4A4 linear layer on B200 (sm_100a).
 
 Argument marshalling only: every function below checks tensor placement, dtype and
-contiguity, allocates outputs with torch when the caller does not pass them, and calls the
+contiguity, allocates outputs (on the call's stream) when the caller does not pass them, and calls the
 C entry point of the same name in ``_build/libmacaq.so`` with the tensors' device made
 current, on that device's current CUDA stream (or the stream passed, which must belong to it).  All
 arithmetic runs in the library's CUDA kernels; there is no CPU or PyTorch fallback -- if
@@ -196,6 +196,22 @@ def _need_numel(t: torch.Tensor, name: str, n: int) -> None:
         raise ValueError(f"{name} holds {t.numel()} elements, the call needs at least {n}")
 
 
+def _empty(shape, dtype: torch.dtype, device: torch.device, stream) -> torch.Tensor:
+    """Memory for a call on `stream` (None: the current one).  Of another stream than the current it is that
+    stream's own, so the kernels there meet neither what the current stream still does with memory given back before,
+    nor what it gets when a workspace is dropped at the end of the call; and a result that the caller drops is not
+    used again before the current stream is done with it, too."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    _check_stream_device(stream, device)
+    here = torch.cuda.current_stream(device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if here != stream:
+        t.record_stream(here)
+    return t
+
+
 def scale_bytes(rows: int, K: int) -> int:
     """Size of an E8M0 scale buffer in the MMA tile layout (include/macaq.h)."""
     return int(load_library().macaq_scale_bytes(rows, K))
@@ -223,7 +239,7 @@ def macaq_scales_to_tiled(rowmajor: torch.Tensor, K: int, tiled=None, stream=Non
     rows = rowmajor.shape[0]
     _need(rowmajor, "rowmajor", torch.uint8, (rows, K // 32))
     dev = rowmajor.device
-    tiled = torch.empty(scale_bytes(rows, K), dtype=torch.uint8, device=dev) if tiled is None else tiled
+    tiled = _empty(scale_bytes(rows, K), torch.uint8, dev, stream) if tiled is None else tiled
     _need(tiled, "tiled", torch.uint8, min_numel=scale_bytes(rows, K), device=dev)
     with torch.cuda.device(dev):
         _check(load_library().macaq_scales_to_tiled(_ptr(rowmajor), rows, K, _ptr(tiled), _stream(stream, dev)),
@@ -235,7 +251,7 @@ def macaq_scales_to_rowmajor(tiled: torch.Tensor, rows: int, K: int, rowmajor=No
     """MMA-tile-layout E8M0 scales -> row-major uint8 [rows, K/32]."""
     _need(tiled, "tiled", torch.uint8, min_numel=scale_bytes(rows, K))
     dev = tiled.device
-    rowmajor = torch.empty(rows, K // 32, dtype=torch.uint8, device=dev) if rowmajor is None else rowmajor
+    rowmajor = _empty((rows, K // 32), torch.uint8, dev, stream) if rowmajor is None else rowmajor
     _need(rowmajor, "rowmajor", torch.uint8, (rows, K // 32), device=dev)
     with torch.cuda.device(dev):
         _check(load_library().macaq_scales_to_rowmajor(_ptr(tiled), rows, K, _ptr(rowmajor), _stream(stream, dev)),
@@ -252,7 +268,7 @@ def macaq_calibrate_scale(xcal: torch.Tensor, W: torch.Tensor, s=None, stream=No
     N = W.shape[0]
     if W.shape[1] != K:
         raise ValueError("xcal and W must have the same K")
-    s = torch.empty(K, dtype=torch.float32, device=W.device) if s is None else s
+    s = _empty(K, torch.float32, W.device, stream) if s is None else s
     _need(s, "s", torch.float32, (K,), device=W.device)
     with torch.cuda.device(dev):
         _check(load_library().macaq_calibrate_scale(_ptr(xcal), C, _ptr(W), N, K, _ptr(s), _stream(stream, dev)),
@@ -266,9 +282,9 @@ def macaq_fold_weights(W: torch.Tensor, s: torch.Tensor, Wq=None, Ws=None, act_m
     _need(W, "W", torch.float32)
     dev = W.device
     _need(s, "s", torch.float32, (K,), device=dev)
-    Wq = torch.empty(N, K // 2, dtype=torch.uint8, device=dev) if Wq is None else Wq
-    Ws = torch.empty(max(scale_bytes(N, K), 1), dtype=torch.uint8, device=dev) if Ws is None else Ws
-    act_mult = torch.empty(K, dtype=torch.float32, device=dev) if act_mult is None else act_mult
+    Wq = _empty((N, K // 2), torch.uint8, dev, stream) if Wq is None else Wq
+    Ws = _empty(max(scale_bytes(N, K), 1), torch.uint8, dev, stream) if Ws is None else Ws
+    act_mult = _empty(K, torch.float32, dev, stream) if act_mult is None else act_mult
     _need(Wq, "Wq", torch.uint8, (N, K // 2), device=dev)
     _need(Ws, "Ws", torch.uint8, min_numel=scale_bytes(N, K), device=dev)
     _need(act_mult, "act_mult", torch.float32, (K,), device=dev)
@@ -284,8 +300,8 @@ def macaq_act_transform_quant(x: torch.Tensor, act_mult: torch.Tensor, Aq=None, 
     _need(x, "x", torch.bfloat16)
     dev = x.device
     _need(act_mult, "act_mult", torch.float32, (K,), device=dev)
-    Aq = torch.empty(M, K // 2, dtype=torch.uint8, device=dev) if Aq is None else Aq
-    As = torch.empty(max(scale_bytes(M, K), 1), dtype=torch.uint8, device=dev) if As is None else As
+    Aq = _empty((M, K // 2), torch.uint8, dev, stream) if Aq is None else Aq
+    As = _empty(max(scale_bytes(M, K), 1), torch.uint8, dev, stream) if As is None else As
     _need(Aq, "Aq", torch.uint8, (M, K // 2), device=dev)
     _need(As, "As", torch.uint8, min_numel=scale_bytes(M, K), device=dev)
     with torch.cuda.device(dev):
@@ -299,8 +315,8 @@ def macaq_act_quant_plain(x: torch.Tensor, Aq=None, As=None, stream=None):
     M, K = x.shape
     _need(x, "x", torch.bfloat16)
     dev = x.device
-    Aq = torch.empty(M, K // 2, dtype=torch.uint8, device=dev) if Aq is None else Aq
-    As = torch.empty(max(scale_bytes(M, K), 1), dtype=torch.uint8, device=dev) if As is None else As
+    Aq = _empty((M, K // 2), torch.uint8, dev, stream) if Aq is None else Aq
+    As = _empty(max(scale_bytes(M, K), 1), torch.uint8, dev, stream) if As is None else As
     _need(Aq, "Aq", torch.uint8, (M, K // 2), device=dev)
     _need(As, "As", torch.uint8, min_numel=scale_bytes(M, K), device=dev)
     with torch.cuda.device(dev):
@@ -320,12 +336,12 @@ def macaq_mxfp4_gemm(Aq, As, Wq, Ws, M: int, N: int, K: int, y=None, out_fp32: b
     _need(As, "As", torch.uint8, min_numel=scale_bytes(M, K), device=dev)
     _need(Ws, "Ws", torch.uint8, min_numel=scale_bytes(N, K), device=dev)
     dt = torch.float32 if out_fp32 else torch.bfloat16
-    y = torch.empty(M, N, dtype=dt, device=dev) if y is None else y
+    y = _empty((M, N), dt, dev, stream) if y is None else y
     _need(y, "y", dt, (M, N), device=dev)
     if data_parallel:
         workspace = None
     elif workspace is None:
-        workspace = torch.empty(max(gemm_workspace_bytes(M, N, K, dev), 1), dtype=torch.uint8, device=dev)
+        workspace = _empty(max(gemm_workspace_bytes(M, N, K, dev), 1), torch.uint8, dev, stream)
     if workspace is not None:
         _need(workspace, "workspace", torch.uint8, device=dev)
     with torch.cuda.device(dev):
@@ -345,10 +361,10 @@ def macaq_w4a4_linear(x: torch.Tensor, act_mult: torch.Tensor, Wq: torch.Tensor,
     _need(act_mult, "act_mult", torch.float32, (K,), device=dev)
     _need(Wq, "Wq", torch.uint8, (N, K // 2), device=dev)
     _need(Ws, "Ws", torch.uint8, min_numel=scale_bytes(N, K), device=dev)
-    y = torch.empty(M, N, dtype=torch.bfloat16, device=dev) if y is None else y
+    y = _empty((M, N), torch.bfloat16, dev, stream) if y is None else y
     _need(y, "y", torch.bfloat16, (M, N), device=dev)
     need = linear_workspace_bytes(M, N, K, dev)
-    workspace = torch.empty(need, dtype=torch.uint8, device=dev) if workspace is None else workspace
+    workspace = _empty(need, torch.uint8, dev, stream) if workspace is None else workspace
     _need(workspace, "workspace", torch.uint8, device=dev)
     with torch.cuda.device(dev):
         _check(load_library().macaq_w4a4_linear(_ptr(x), M, K, _ptr(act_mult), _ptr(Wq), _ptr(Ws), N, _ptr(y),
@@ -365,10 +381,10 @@ def macaq_mxfp4_linear(x: torch.Tensor, Wq: torch.Tensor, Ws: torch.Tensor, N: i
     dev = x.device
     _need(Wq, "Wq", torch.uint8, (N, K // 2), device=dev)
     _need(Ws, "Ws", torch.uint8, min_numel=scale_bytes(N, K), device=dev)
-    y = torch.empty(M, N, dtype=torch.bfloat16, device=dev) if y is None else y
+    y = _empty((M, N), torch.bfloat16, dev, stream) if y is None else y
     _need(y, "y", torch.bfloat16, (M, N), device=dev)
     need = linear_workspace_bytes(M, N, K, dev)
-    workspace = torch.empty(need, dtype=torch.uint8, device=dev) if workspace is None else workspace
+    workspace = _empty(need, torch.uint8, dev, stream) if workspace is None else workspace
     _need(workspace, "workspace", torch.uint8, device=dev)
     with torch.cuda.device(dev):
         _check(load_library().macaq_mxfp4_linear(_ptr(x), M, K, _ptr(Wq), _ptr(Ws), N, _ptr(y), _ptr(workspace),
@@ -400,10 +416,10 @@ def macaq_w4a4_linear_multi(x: torch.Tensor, act_mult, Wq: torch.Tensor, Ws: tor
         _need(act_mult, "act_mult", torch.float32, (G, K), device=dev)
     _need(Wq, "Wq", torch.uint8, (Nt, K // 2), device=dev)
     _need(Ws, "Ws", torch.uint8, min_numel=sum(scale_bytes(int(v), K) for v in n), device=dev)
-    y = torch.empty(M, Nt, dtype=torch.bfloat16, device=dev) if y is None else y
+    y = _empty((M, Nt), torch.bfloat16, dev, stream) if y is None else y
     _need(y, "y", torch.bfloat16, (M, Nt), device=dev)
     need = linear_multi_workspace_bytes(M, G, K, dev)
-    workspace = torch.empty(need, dtype=torch.uint8, device=dev) if workspace is None else workspace
+    workspace = _empty(need, torch.uint8, dev, stream) if workspace is None else workspace
     _need(workspace, "workspace", torch.uint8, device=dev)
     with torch.cuda.device(dev):
         _check(load_library().macaq_w4a4_linear_multi(_ptr(x), M, K, G, _ptr(act_mult), _ptr(Wq), _ptr(Ws),
@@ -441,10 +457,10 @@ def macaq_w4a4_grouped_linear(x: torch.Tensor, counts, act_mult, Wq: torch.Tenso
         _need(act_mult, "act_mult", torch.float32, (E, K), device=dev)
     _need(Wq, "Wq", torch.uint8, (E, N, K // 2), device=dev)
     _need(Ws, "Ws", torch.uint8, min_numel=E * scale_bytes(N, K), device=dev)
-    y = torch.empty(T, N, dtype=torch.bfloat16, device=dev) if y is None else y
+    y = _empty((T, N), torch.bfloat16, dev, stream) if y is None else y
     _need(y, "y", torch.bfloat16, (T, N), device=dev)
     need = max(grouped_workspace_bytes(c, N, K), 1)
-    workspace = torch.empty(need, dtype=torch.uint8, device=dev) if workspace is None else workspace
+    workspace = _empty(need, torch.uint8, dev, stream) if workspace is None else workspace
     _need(workspace, "workspace", torch.uint8, device=dev)
     with torch.cuda.device(dev):
         _check(load_library().macaq_w4a4_grouped_linear(_ptr(x), cp, E, K, _ptr(act_mult), _ptr(Wq), _ptr(Ws), N,
@@ -478,12 +494,12 @@ def macaq_w4a4_grouped_linear_device(x: torch.Tensor, counts: torch.Tensor, act_
         _need(act_mult, "act_mult", torch.float32, (E, K), device=dev)
     _need(Wq, "Wq", torch.uint8, (E, N, K // 2), device=dev)
     _need(Ws, "Ws", torch.uint8, min_numel=E * scale_bytes(N, K), device=dev)
-    y = torch.empty(T, N, dtype=torch.bfloat16, device=dev) if y is None else y
+    y = _empty((T, N), torch.bfloat16, dev, stream) if y is None else y
     _need(y, "y", torch.bfloat16, (T, N), device=dev)
     need = grouped_device_workspace_bytes(T, E, N, K, dev)
     if need == 0:
         raise ValueError("shape not supported by the grouped linear (1 <= E <= 128, N % 128 == 0, T >= 1)")
-    workspace = torch.empty(need, dtype=torch.uint8, device=dev) if workspace is None else workspace
+    workspace = _empty(need, torch.uint8, dev, stream) if workspace is None else workspace
     _need(workspace, "workspace", torch.uint8, min_numel=need, device=dev)
     with torch.cuda.device(dev):
         _check(load_library().macaq_w4a4_grouped_linear_device(
@@ -508,7 +524,7 @@ def macaq_w4a4_linear_noalloc(x: torch.Tensor, act_mult: torch.Tensor, Wq: torch
     _need(act_mult, "act_mult", torch.float32, (K,), device=dev)
     _need(Wq, "Wq", torch.uint8, (N, K // 2), device=dev)
     _need(Ws, "Ws", torch.uint8, min_numel=scale_bytes(N, K), device=dev)
-    y = torch.empty(M, N, dtype=torch.bfloat16, device=dev) if y is None else y
+    y = _empty((M, N), torch.bfloat16, dev, stream) if y is None else y
     _need(y, "y", torch.bfloat16, (M, N), device=dev)
     with torch.cuda.device(dev):
         _check(load_library().macaq_w4a4_linear_noalloc(_ptr(x), M, K, _ptr(act_mult), _ptr(Wq), _ptr(Ws), N, _ptr(y),
@@ -523,10 +539,10 @@ def macaq_calib_hessian(xcal: torch.Tensor, act_mult: torch.Tensor, Hs=None, wor
     _need(xcal, "xcal", torch.bfloat16)
     dev = xcal.device
     _need(act_mult, "act_mult", torch.float32, (K,), device=dev)
-    Hs = torch.empty(K, K, dtype=torch.float64, device=dev) if Hs is None else Hs
+    Hs = _empty((K, K), torch.float64, dev, stream) if Hs is None else Hs
     _need(Hs, "Hs", torch.float64, (K, K), device=dev)
     need = int(load_library().macaq_hessian_workspace_bytes(C, K))
-    workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev) if workspace is None else workspace
+    workspace = _empty(max(need, 1), torch.uint8, dev, stream) if workspace is None else workspace
     _need(workspace, "workspace", torch.uint8, min_numel=need, device=dev)
     with torch.cuda.device(dev):
         _check(load_library().macaq_calib_hessian(_ptr(xcal), C, K, _ptr(act_mult), _ptr(Hs), _ptr(workspace),
@@ -545,12 +561,12 @@ def macaq_flip_refine(W: torch.Tensor, s: torch.Tensor, Hs: torch.Tensor, Wq: to
     _need(Hs, "Hs", torch.float64, (K, K), device=dev)
     _need(Wq, "Wq", torch.uint8, (N, K // 2), device=dev)
     _need(Ws, "Ws", torch.uint8, min_numel=scale_bytes(N, K), device=dev)
-    moves = torch.empty(N, dtype=torch.int32, device=dev) if moves is None else moves
+    moves = _empty(N, torch.int32, dev, stream) if moves is None else moves
     _need(moves, "moves", torch.int32, (N,), device=dev)
     need = int(load_library().macaq_flip_refine_workspace_bytes(N, K))
     if need == 0:
         raise ValueError(f"K={K} is not supported by macaq_flip_refine (K <= 12288, K % 32 == 0)")
-    workspace = torch.empty(need, dtype=torch.uint8, device=dev) if workspace is None else workspace
+    workspace = _empty(need, torch.uint8, dev, stream) if workspace is None else workspace
     _need(workspace, "workspace", torch.uint8, min_numel=need, device=dev)
     with torch.cuda.device(dev):
         _check(load_library().macaq_flip_refine(_ptr(W), N, K, _ptr(s), _ptr(Hs), _ptr(Wq), _ptr(Ws), int(max_moves),
@@ -559,10 +575,10 @@ def macaq_flip_refine(W: torch.Tensor, s: torch.Tensor, Hs: torch.Tensor, Wq: to
     return moves
 
 
-def _out(t, name: str, shape, like: torch.Tensor) -> torch.Tensor:
+def _out(t, name: str, shape, like: torch.Tensor, stream) -> torch.Tensor:
     """A bf16 result on the device of `like`: the caller's tensor after its checks, or a new one."""
     if t is None:
-        return like.new_empty(shape, dtype=torch.bfloat16)
+        return _empty(shape, torch.bfloat16, like.device, stream)
     _need(t, name, torch.bfloat16, shape, device=like.device)
     return t
 
@@ -631,8 +647,8 @@ def macaq_qk_norm_rope(qkv: torch.Tensor, Hq: int, Hk: int, head_dim: int, rope=
     for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
         if w is not None:
             _need(w, name, torch.float32, (head_dim,), device=dev)
-    q = _out(q, "q", (T, Hq, head_dim), qkv)
-    k = _out(k, "k", (T, Hk, head_dim), qkv)
+    q = _out(q, "q", (T, Hq, head_dim), qkv, stream)
+    k = _out(k, "k", (T, Hk, head_dim), qkv, stream)
     with _device(dev):
         _check(load_library().macaq_qk_norm_rope(_ptr(qkv), T, ld, Hq, Hk, head_dim, _ptr(q_weight), _ptr(k_weight),
                                                  eps, _ptr(rope), rows, R, 1 if interleaved else 0, _ptr(positions),
@@ -659,7 +675,7 @@ def macaq_kv4_append(qkv: torch.Tensor, Hq: int, Hk: int, head_dim: int, cache: 
         if w is not None:
             _need(w, name, torch.float32, (head_dim,), device=dev)
     if Hq:
-        q = _out(q, "q", (T, Hq, head_dim), qkv)
+        q = _out(q, "q", (T, Hq, head_dim), qkv, stream)
     with _device(dev):
         _check(load_library().macaq_kv4_append(_ptr(qkv), T, ld, Hq, Hk, head_dim, _ptr(q_weight), _ptr(k_weight), eps,
                                                _ptr(rope), rows, R, 1 if interleaved else 0, _ptr(positions),
@@ -676,8 +692,8 @@ def macaq_kv4_gather(cache: torch.Tensor, head_dim: int, page_size: int, slots: 
     dev = cache.device
     T = slots.numel()
     _need(slots, "slots", torch.int64, (T,), device=dev)
-    k = _out(k, "k", (T, Hk, head_dim), cache)
-    v = _out(v, "v", (T, Hk, head_dim), cache)
+    k = _out(k, "k", (T, Hk, head_dim), cache, stream)
+    v = _out(v, "v", (T, Hk, head_dim), cache, stream)
     with _device(dev):
         _check(load_library().macaq_kv4_gather(_ptr(cache), pages, page_size, Hk, head_dim, _ptr(slots), T, _ptr(k),
                                                _ptr(v), _stream(stream, dev)), "macaq_kv4_gather")
@@ -719,14 +735,14 @@ def macaq_kv4_attention(q: torch.Tensor, cache: torch.Tensor, page_size: int, ta
         _need(cu_q, "cu_q", torch.int32, (B + 1,), device=dev)
     elif B != T or max_q != 1:
         raise ValueError("without cu_q every sequence has one query: T = B and max_q = 1")
-    out = _out(out, "out", (T, Hq, D), q)
+    out = _out(out, "out", (T, Hq, D), q, stream)
     if lse is not None:
         _need(lse, "lse", torch.float32, (T, Hq), device=dev)
     need = kv4_attention_workspace_bytes(T, B, Hq, Hk, D, max_q, dev)
     if need == 0:
         raise ValueError("shape not supported by the attention (Hq a multiple of Hk, at most 1024; max_q >= 1)")
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        workspace = _empty(need, torch.uint8, dev, stream)
     else:
         _need(workspace, "workspace", torch.uint8, min_numel=need, device=dev)
     with _device(dev):
