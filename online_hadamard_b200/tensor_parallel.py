@@ -68,10 +68,16 @@ def tp_w4a4_linear(x: torch.Tensor, act_mult: torch.Tensor, Wq_shard: torch.Tens
                    N: int, group=None, workspace=None, stream=None) -> torch.Tensor:
     """y = x W^T over the ranks of `group`: this rank's W4A4 linear on its weight shard (from
     shard_folded_weights), then the all-gather of the output columns."""
-    from . import macaq_w4a4_linear
+    from . import _check_stream_device, macaq_w4a4_linear
+    if stream is not None:  # the gather belongs behind the linear, on the same stream
+        _check_stream_device(stream, x.device)
+        here = torch.cuda.current_stream(x.device)
+        with torch.cuda.stream(stream):
+            y = tp_w4a4_linear(x, act_mult, Wq_shard, Ws_shard, N, group, workspace)
+        y.record_stream(here)
+        return y
     if Wq_shard.shape[0] == 0:  # more ranks than 128-row blocks: nothing to compute here
         y_shard = torch.empty(x.shape[0], 0, dtype=torch.bfloat16, device=x.device)
     else:
-        y_shard = macaq_w4a4_linear(x, act_mult, Wq_shard, Ws_shard, Wq_shard.shape[0], workspace=workspace,
-                                    stream=stream)
+        y_shard = macaq_w4a4_linear(x, act_mult, Wq_shard, Ws_shard, Wq_shard.shape[0], workspace=workspace)
     return gather_columns(y_shard, N, group)

@@ -134,3 +134,18 @@ def test_a_stream_of_its_own_inside_a_graph(mq):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, want)
+
+
+def test_the_gather_of_a_split_linear_follows_it_on_its_stream(mq, monkeypatch):
+    from online_hadamard_b200 import tensor_parallel as tp
+    g = torch.Generator().manual_seed(61)
+    x = torch.randn(40, 512, generator=g).to(torch.bfloat16).cuda()
+    Wq, Ws, am = mq.macaq_fold_weights((torch.randn(256, 512, generator=g) * 0.05).cuda(), torch.ones(512).cuda())
+    want = mq.macaq_w4a4_linear(x, am, Wq, Ws, 256)
+    at = []
+    monkeypatch.setattr(tp, "gather_columns", lambda y, N, group=None: at.append(torch.cuda.current_stream()) or y)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    y = tp.tp_w4a4_linear(x, am, Wq, Ws, 256, stream=side)
+    side.synchronize()
+    assert at == [side] and torch.equal(y, want)
