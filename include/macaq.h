@@ -393,7 +393,8 @@ int macaq_qk_norm_rope(const uint16_t* qkv, int64_t T, int64_t ld, int Hq, int H
  *   cache  in/out  as above; only the bytes of the slots' tokens are written
  *   slots  in      int64 [T]; negative: the row is padding, its key and value are not stored.  Two rows
  *                  of one call must not name the same slot (its bytes would be a mix of both)
- *   q      out     bf16 [T][Hq][D], written for padding rows too; not overlapping qkv
+ *   q      out     bf16 [T][Hq][D], written for padding rows too (zeros where their position is outside the
+ *                  table, which is not reported for them); not overlapping qkv
  * The codes come from fp32 arithmetic in one canonical order, one rounding per operation: the sum of squares
  * adds neighbours first (distances 1, 2, 4, .. D/2), y = fl(fl(x r) w), rotation fl(fl(y_i c) - fl(y_j s)).
  */

@@ -184,7 +184,8 @@ __device__ __forceinline__ void run_head_units(const HeadParams& p, int64_t bloc
     if (t >= p.T) return;
     bool ok = true;
     const float* trow = angles_of(p, t, ok);
-    if (!ok) {
+    const bool padding = !ok && p.slots && p.slots[t] < 0;  // any position will do there: zeros
+    if (!ok && !padding) {
         report_index();
         return;
     }
@@ -196,6 +197,10 @@ __device__ __forceinline__ void run_head_units(const HeadParams& p, int64_t bloc
     const int n = min(p.heads_per_unit, heads - h0);
     const uint16_t* src = p.qkv + t * p.ld + static_cast<int64_t>((is_k ? p.Hq : 0) + h0) * D;
     uint16_t* dst = (is_k ? p.k : p.q) + (t * heads + h0) * D;
+    if (padding) {
+        for (int i = l; i < n * (D / 8); i += kLanes) reinterpret_cast<uint4*>(dst)[i] = make_uint4(0, 0, 0, 0);
+        return;
+    }
     head_unit<D, MODE>(src, dst, n, is_k ? p.wk : p.wq, p.eps, trow, p.R, l);
 }
 

@@ -199,3 +199,32 @@ def test_gather_reports_slots_outside_the_cache(mq):
     assert k[0].any() and not k[1:].any() and not v[1:].any()
     k, v = mq.macaq_kv4_gather(cache, 64, 16, cuda(np.array([31, -5])))
     assert mq.macaq_device_status() == 0
+
+
+@pytest.mark.parametrize("T,Hq,Hk,D,R,inter", [(6, 3, 1, 64, 64, False), (9, 16, 2, 128, 64, True), (400, 40, 4, 128, 128, False)])
+def test_padding_rows_need_no_position(mq, T, Hq, Hk, D, R, inter):
+    """Rows of negative slots whose positions are outside the table, as padding often has them: zero queries, nothing
+    stored and nothing reported; with a position of the table they are normed and rotated as before."""
+    rng = np.random.default_rng(T)
+    x, table = rows(rng, T, (Hq + 2 * Hk) * D), rope_table(50, R)
+    w = (rng.random(D) + 0.5).astype(np.float32)
+    pos = rng.integers(0, 50, T)
+    slots = rng.permutation(T + 32)[:T]
+    pad = rng.permutation(T)[:max(3, T // 4)]
+    slots[pad] = -1
+    pos[pad[:-1]] = rng.choice([-1, 50, 2 ** 40, -2 ** 62], len(pad) - 1)
+    page = 32
+    cache = torch.zeros((T + 63) // page + 1, Hk, mq.kv4_page_bytes(page, D), dtype=torch.uint8, device="cuda")
+    q = torch.full((T, Hq, D), 7.0, dtype=torch.bfloat16, device="cuda")
+    mq.macaq_device_status(clear=True)
+    mq.macaq_kv4_append(cuda(x, torch.bfloat16), Hq, Hk, D, cache, page, cuda(slots), cuda(table), cuda(pos), q_weight=cuda(w),
+                        eps=EPS, interleaved=inter, q=q)
+    assert mq.macaq_device_status(clear=True) == 0
+    assert not q[torch.from_numpy(pad[:-1])].any()
+    keep = np.setdiff1d(np.arange(T), pad[:-1])
+    h = x.reshape(T, Hq + 2 * Hk, D)
+    check_heads(q[torch.from_numpy(keep)], h[keep, :Hq], w, table[pos[keep]], R, inter)
+    want = np.zeros(cache.shape, np.uint8)
+    real = np.flatnonzero(slots >= 0)
+    kv.store(want, slots[real], page, kv.norm_rope(h[real, Hq:Hq + Hk], None, EPS, table[pos[real]], R, inter), h[real, Hq + Hk:])
+    assert np.array_equal(cache.cpu().numpy(), want)
