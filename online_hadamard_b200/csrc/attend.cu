@@ -1811,14 +1811,19 @@ __global__ void __launch_bounds__(128) attend_join_kernel(const __grid_constant_
 constexpr int64_t kMaxKeys = int64_t{1} << 30;  // of a sequence: positions and block ends stay in 32 bits
 
 // How a call is split, from what the host knows (not the sequences' lengths).
-// attend_few_kernel takes up to 16 query rows of a unit always, and up to kFewMost where tables are longer than
-// kWholeKeys keys and, for heads of 128, there are kFewUnits pairs of a sequence and a kv head: its 32-row tiles
-// are bound by latency, the tiles of 256 of attend_many_kernel by the empty rows.  Measured, 32 rows (4 queries, 8
-// heads a kv head, 8 kv heads), few against many: heads of 128, 4000 keys, 8 sequences 73 / 64 us, 16 96 / 105 us,
-// 24 118 / 142 us; 64 of 300 keys 99 / 65 us; heads of 64, 4000 keys, 8 sequences 44 / 58 us.  64 rows (24 sequences
-// of 4000 keys, tiles of 32 read the keys twice): 202 / 144 us.
+// attend_few_kernel takes up to 16 query rows of a unit always; up to kFewMost for heads of 64, and for heads of 128 where
+// the sequences' tables (or windows) and kv heads together have room for kFewKeys keys: its 32-row tiles are bound by
+// latency, the tiles of 256 of attend_many_kernel by the empty rows.  Device times of a call, few against many, 1 to 64
+// sequences of 300 to 16000 keys, 1 and 8 kv heads, 20 and 32 rows, equal and ragged lengths, a window of 1024:
+//   heads of 64    few faster in 55 of 76 cases, up to 2.3 times (24 sequences of 300 keys, 8 kv heads: 21.5 / 37.6 us),
+//                  many in the others up to 1.14 times (one sequence of 4000: 26.7 / 23.8 us)
+//   heads of 128   8 kv heads, 4 sequences of 4000: 44.7 / 44.9 us, 12: 83.7 / 87.3, 24: 120 / 143, 64: 253 / 340; 4 of 16000: 88 / 98;
+//                  1 kv head, 24 of 16000: 80 / 79, 64: 133 / 175; below some 2^19 keys many is faster (64 sequences of 4000,
+//                  1 kv head: 73 / 66; 1 to 24 of 300: 37 / 26).  What the host does not see are ragged lengths: 24 sequences
+//                  of 500 to 4000 keys, 8 kv heads, 118 / 96 us, are taken for full ones.
+// 64 rows (24 sequences of 4000 keys, tiles of 32 read the keys twice): 202 / 144 us.
 constexpr int kFewMost = 32;
-constexpr int kFewUnits = 96;
+constexpr int64_t kFewKeys = int64_t{1} << 19;
 // Keys of a sequence's table up to which few rows are not cut (one query, 64 heads on 8: 48 sequences of 500 keys 14.8
 // against 23.5 us, 32 of 1000 keys 19.9 against 23.9 us, one of 1000 keys 13.4 against 12.5 us).
 constexpr int64_t kWholeKeys = 1024;
@@ -1827,10 +1832,11 @@ struct AttendPlan {
     int64_t units;
     size_t bytes;
 };
-static AttendPlan plan_attend(int64_t B, int Hq, int Hk, int D, int64_t max_q, int64_t keys) {
+static AttendPlan plan_attend(int64_t B, int Hq, int Hk, int D, int64_t max_q, int64_t keys, int64_t window) {
     AttendPlan a = {};
     const int64_t rows = max_q * (Hq / Hk);
-    const bool few32 = rows <= kFewMost && keys > kWholeKeys && (D == 64 || B * Hk >= kFewUnits);
+    const int64_t seen = window && window < keys - max_q ? window + max_q : keys;
+    const bool few32 = rows <= kFewMost && (D == 64 || (seen > 0 && B * Hk >= (kFewKeys + seen - 1) / seen));
     a.tile_rows = rows <= 8 ? 8 : rows <= 16 ? 16 : few32 ? 32 : kManyRows;
     a.row_tiles = static_cast<int>((rows + a.tile_rows - 1) / a.tile_rows);
     if (B > kMaxDim / (static_cast<int64_t>(Hk) * a.row_tiles)) return a;  // units are counted in 31 bits
@@ -1901,8 +1907,8 @@ extern "C" size_t macaq_kv4_attention_workspace_bytes(int64_t T, int64_t B, int 
         return 0;
     if (T == 0 || B == 0) return 256;
     // whatever the tables' width
-    const size_t a = plan_attend(B, Hq, Hk, head_dim, max_q, 0).bytes;
-    const size_t z = plan_attend(B, Hq, Hk, head_dim, max_q, kMaxKeys).bytes;
+    const size_t a = plan_attend(B, Hq, Hk, head_dim, max_q, 0, 0).bytes;
+    const size_t z = plan_attend(B, Hq, Hk, head_dim, max_q, kMaxKeys, 0).bytes;
     return a && z ? (a > z ? a : z) : 0;
 }
 
@@ -1925,7 +1931,7 @@ extern "C" int macaq_kv4_attention(const uint16_t* q, int64_t T, int64_t ldq, in
         (reinterpret_cast<uintptr_t>(cu_q) & 3u) || (reinterpret_cast<uintptr_t>(lse) & 3u))
         return MACAQ_EALIGN;
     if (workspace_bytes < need) return MACAQ_EWORKSPACE;
-    const AttendPlan plan = plan_attend(B, Hq, Hk, head_dim, max_q, table_width * page_size);
+    const AttendPlan plan = plan_attend(B, Hq, Hk, head_dim, max_q, table_width * page_size, window);
     AttendParams p = {};
     p.q = q, p.T = T, p.ldq = ldq, p.Hq = Hq, p.Hk = Hk, p.G = Hq / Hk, p.cache = cache, p.num_pages = num_pages;
     p.page_size = page_size, p.page_shift = __builtin_ctz(page_size), p.tables = tables, p.table_width = table_width;

@@ -12,7 +12,7 @@ pytestmark = pytest.mark.gpu
 # (D, query heads a kv head, queries a sequence, kv heads, page, keys the tables have room for): 8, 16 and 32 rows of the
 # kernel of few rows, tables that are cut and that are not, and the kernel of many rows
 KERNELS = [(128, 2, 3, 2, 32, 0), (64, 4, 4, 1, 16, 0), (128, 8, 2, 1, 64, 2000), (64, 8, 4, 1, 32, 2000),
-           (128, 2, 40, 2, 16, 0), (64, 1, 300, 1, 64, 0)]
+           (128, 8, 4, 1, 64, 1 << 19), (128, 2, 40, 2, 16, 0), (64, 1, 300, 1, 64, 0)]
 
 
 class Cached:
