@@ -272,8 +272,9 @@ __device__ __forceinline__ int wide_reference(int top) { return max(top - 70, 1)
 // largest scale a warp has met.  Each warp copies its own blocks, kStages deep, with nothing shared
 // until the end, where the warps' sums are joined.
 //
-// Measured (heads of 128, 64 on 8): 16 sequences of 32768 keys, 570 MB of cache, 123 us, 4.6 TB/s; 32 on 8, 32
-// sequences of up to 8000 keys (157 MB), 45 us, 3.5 TB/s.  A strip of 16 tokens takes about 284 warp
+// Measured (heads of 128, 64 on 8; the kernel and the joining one, in a captured graph): 16 sequences of 32768 keys, 570 MB
+// of cache, 121 us, 4.7 TB/s; 32 on 8, 32 sequences of up to 8000 keys (157 MB), 47 us, 3.3 TB/s.  The public call takes
+// 121 to 133 and 45 to 49 us.  A strip of 16 tokens takes about 284 warp
 // instructions (a conversion per two codes, 64, and 32 matrix instructions and their scales among them); they fill 56 %
 // of the issue slots of three CTAs an SM.  Four CTAs (128 registers, spilling) issue no more; one strip at a time
 // is 9 % slower, as two in flight hide each other's latencies; a CTA's start and end cost some 15 us in all.
@@ -827,9 +828,9 @@ __global__ void __launch_bounds__(kFewThreads, few_resident(NT)) attend_few_kern
 // as long that way, 2.8 times in all (prompt of 8192 tokens, a value 2^40 times larger in each head: 0.64 / 1.8 ms).  A
 // branch in the roles' loops instead, or the look at the scales in the role that widens V, cost every call 15 % and more.
 //
-// Measured: a prompt of 8192 tokens, 32 heads of 128 on 8, 605 us, 910 TFLOP/s of the pairs the mask leaves (tensor
-// pipe half busy).  Neither the exponentials (replaced by a product: 583 us) nor the widening (left out: 577 us) bound
-// it, but the chain scores - maximum - weights - products of a tile with only two softmax warps a scheduler to hide it.
+// Measured: a prompt of 8192 tokens, 32 heads of 128 on 8, 639 us with the joining kernel in a captured graph, 860 TFLOP/s
+// of the pairs the mask leaves (tensor pipe less than half busy); the public call takes 640 to 680 us.  When this kernel
+// alone took 605 us, neither the exponentials (replaced by a product: 583 us) nor the widening (left out: 577 us) bound it, but the chain scores - maximum - weights - products of a tile with only two softmax warps a scheduler to hide it.
 // On the way there: products issued by a thread that the compiler did not know to be one 1713 us, by a converged
 // warp 1310; code cut so that the roles' loops fit the instruction cache 718; scores of half blocks ahead, two issuing
 // warps 640.  Letting the two tiles' exponentials take turns cost 3 %.
@@ -1844,7 +1845,10 @@ static AttendPlan plan_attend(int64_t B, int Hq, int Hk, int D, int64_t max_q, i
     if (a.tile_rows == kManyRows) {
         a.ctas = sm_count();
         a.unit_cost = 4;
-    } else {  // cut while there are few units: many balance themselves, and need no joining
+    } else {
+        // Cut while there are few units.  Many fill the GPU whole, and need no joining (256 sequences of 4000 keys, 64
+        // heads on 8: 232 / 251 us; of 500 to 4000 keys, four queries, 32 on 8: 253 / 288) unless one is far longer than
+        // all others, which the host does not see (300 sequences of 200 keys and one of 100000: 601 / 84 us).
         const int resident = sm_count() * few_resident(a.tile_rows / 8);
         a.ctas = a.units >= 4 * resident || keys <= kWholeKeys ? 0 : resident;
         a.unit_cost = 16;

@@ -6,9 +6,10 @@
 //   cache       MXFP4 (the E8M0 and E2M1 rules of quant.cu) of the unnormalised 32-point
 //               Walsh-Hadamard transform of fl(y_d c0), c0 = fl32(1 / sqrt(32))
 //
-// Everything is fp32 with one rounding per operation.  What reaches the cache runs in one canonical
-// order (the sum of squares adds neighbours first: distances 1, 2, 4, ..), so its codes are
-// reproducible bit for bit; the bf16 outputs are rounded once, from fp32.
+// Everything is fp32.  What reaches the cache runs in one canonical order, one rounding per operation (the sum of
+// squares adds neighbours first: distances 1, 2, 4, ..), so its codes are reproducible bit for bit.  The bf16 outputs
+// are rounded once, from fp32 that sums in the order of its threads and fuses multiplications with additions: the keys
+// of macaq_qk_norm_rope and those that macaq_kv4_append quantises may differ in the last bits of fp32.
 //
 // Work split.  Query heads (and the key heads of macaq_qk_norm_rope): D / 8 lanes own one head, lane
 // l its elements 4l .. 4l+3 of each half, so the pairs (i, i + D/2) meet in one thread and a head's
@@ -17,8 +18,9 @@
 // owns one 32-element block, so the whole transform and quantisation runs in its registers as in
 // quant.cu; the D / 32 threads of a head exchange their sums of squares and code words by shuffles.
 // Both are bound by the bytes of the rows (2 B an element in and out, 17/32 B into the cache).  4096 rows of
-// 64 + 8 heads of 128: norm and rotation 27.4 us (5.6 TB/s), with 8 value heads and the cache 37 us (4.2 TB/s: the
-// threads of the cache's blocks read and transform 64 bytes each, 1000 instructions), reading back 10.4 us.
+// 64 + 8 heads of 128, device time of a call in a captured graph: norm and rotation 29.5 us (5.2 TB/s; the public call
+// takes as long), with 8 value heads and the cache 37.7 us (4.2 TB/s: the threads of the cache's blocks read and
+// transform 64 bytes each, 1000 instructions), reading back 7.0 us (13.5 with the host's call).
 // 64 registers a thread: at 78 the append takes 40 us (30 % of the warps resident), at 48 43 us (spills).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
