@@ -433,7 +433,7 @@ int macaq_kv4_gather(const uint8_t* cache, int64_t num_pages, int page_size, int
  * hold behind a sequence's length, and are the same from run to run.  Rounded to f16 on the way (2^-11): the
  * transformed query, relative to its row's largest element (bits are lost below 2^-26 of it), and the softmax
  * weights.  Values may lie as far apart as they like, seen by a row or not: where a unit of work (a kv head of a
- * sequence and a tile of its query rows) meets V scales more than 2^11 to 2^16 apart, it is done again with weights as
+ * sequence and a tile of its query rows) meets V scales more than 2^11 (2^16 with many rows) apart, it is done again with weights as
  * sums of two bf16, which takes 2 to 3 times as long; values then count down to 2^-196 of the largest of the same
  * 32 elements.  Keys likewise; in the kernel of many query rows, blocks of a key below 2^-26 (2^-10 beside keys 2^16 times as
  * large) of its own largest block count as zero.  An infinity or NaN is stored as values of some 2^126: rows that may not

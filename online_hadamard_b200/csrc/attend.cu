@@ -250,14 +250,15 @@ __device__ __forceinline__ float warp_fwht32(float x, int l) {
     return x;
 }
 
-// Softmax weights are kept in f16 for the second product, relative to a reference within 2^8 of the
+// Softmax weights are kept in f16 for the second product, relative to a reference within 2^5 of the
 // running maximum (it moves only when a score passes it by that much, which is rare, so the sums are
-// seldom rescaled) and times 2^6: at most 2^14, with 11 bits down to 2^-20 of the largest.
-constexpr float kSlack = 8.0f;
-constexpr float kLift = 6.0f;
+// seldom rescaled) and times 2^10: at most 2^15, with 11 bits down to 2^-24 of the largest.  (Within 2^8 and
+// times 2^6 is no faster, and 2^-26 of the largest, all that counts where that one's value is zero, is off by 3 to 8 %.)
+constexpr float kSlack = 5.0f;
+constexpr float kLift = 10.0f;
 
 // Where V's scales lie too far apart for f16, weights times scales are bf16, whose exponents are fp32's, relative to
-// a reference 2^70 below the largest scale of the same 32 elements: 2^70, times 6, a weight of 2^14 and 2^30 keys, stays
+// a reference 2^70 below the largest scale of the same 32 elements: 2^70, times 6, a weight of 2^15 and 2^30 keys, stays
 // below 2^118, and scales down to 2^-196 of the largest are not lost beside it (an infinity is stored as 2^126, so values
 // of 2^-70 count even there).
 __device__ __forceinline__ int wide_reference(int top) { return max(top - 70, 1); }
@@ -279,13 +280,14 @@ __device__ __forceinline__ int wide_reference(int top) { return max(top - 70, 1)
 // of the issue slots of three CTAs an SM.  Four CTAs (128 registers, spilling) issue no more; one strip at a time
 // is 9 % slower, as two in flight hide each other's latencies; a CTA's start and end cost some 15 us in all.
 //
-// V's scale as the exponent of an f16 reaches down to 2^-14 of the reference, which stands up to 2^3 above the largest scale
-// met.  A warp notes the smallest it met, too; where that lies lower (V blocks 2^11 to 2^14 and more apart, and it does
-// not matter which row sees them) the CTA does the unit again, WIDE: weights and scales as bf16, the weights as a sum of
-// two (2^-17 of themselves), relative to a reference of each block of elements.  That is twice the matrix
-// instructions for V and some more for its codes.
+// V's scale goes into the weight, as an f16 relative to a reference up to 2^1 above the largest scale met: with the
+// largest weights 2^10 and more, what a row weighs by 2^-12 of them keeps 11 bits at scales down to 2^-12 of the reference.
+// A warp notes the smallest it met, too; where that lies lower (V blocks 2^12 and more apart, and it does not matter which
+// row sees them) the CTA does the unit again, WIDE: weights and scales as bf16, the weights as a sum of two (2^-17 of
+// themselves), relative to a reference of each block of elements.  That is twice the matrix instructions for V and some
+// more for its codes.
 constexpr int kFewThreads = 128;
-constexpr int kFewSpan = 14;
+constexpr int kFewSpan = 12;
 constexpr int kStages = 3;
 constexpr int kFewShift = 5;
 
@@ -595,8 +597,8 @@ __device__ __forceinline__ bool few_unit(const AttendParams& p, FewShared<D, NT>
             if (__any_sync(0xFFFFFFFFu, grow)) {
                 float vf = 1.0f;
                 const int nv = WIDE ? 0 : static_cast<int>(__reduce_max_sync(0xFFFFFFFFu, static_cast<unsigned>(vtop)));
-                if (!WIDE && nv > vref) {  // with room for three doublings before the next time
-                    const int to = min(nv + 3, 254);
+                if (!WIDE && nv > vref) {  // with room for a doubling before the next time
+                    const int to = min(nv + 1, 254);
                     vf = to - vref < 127 ? __uint_as_float(static_cast<uint32_t>(127 - (to - vref)) << 23) : 0.0f;
                     vref = to;
                 }
@@ -819,7 +821,7 @@ __global__ void __launch_bounds__(kFewThreads, few_resident(NT)) attend_few_kern
 // the softmax reference when it moves), with 2^12 on top, so scales down to 2^-26 of the largest are exact.
 //
 // That is not enough where V's scales lie further apart than 2^kManySpan: blocks vanish, and the weights are f16, too, off by
-// 2^-31 of the largest where they are small, which a value 2^16 larger than the largest weight's makes 2^-15 of that
+// 2^-35 of the largest where they are small, which a value 2^16 larger than the largest weight's makes 2^-19 of that
 // one's share.  Where K's scales lie as far apart, a token can be lost beside another of the 32 that a row may not see
 // or gives no weight.  Warp 19 looks at the units' scales on its own, and when the CTA is through its units it does those again,
 // WIDE, with operands in bf16, whose exponents are fp32's: weights as the sum of two (2^-17 of themselves; the second over

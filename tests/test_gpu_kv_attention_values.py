@@ -195,3 +195,25 @@ def test_keys_that_grow_along_the_sequence(mq, nq):
     k, v, q = sequence(rng, nq + 150, nq, 4, 2, 128)
     k *= np.where(np.arange(len(k)) % 5 == 0, 2.0 ** -40, np.where(np.arange(len(k)) % 7 == 0, 2.0 ** 4, 1.0))[:, None, None]
     Cached([(kv.bf16(k), v, q)], 32).check(mq)
+
+
+@pytest.mark.parametrize("D,G,nq,Hk,page,room", KERNELS)
+@pytest.mark.parametrize("below", [16, 26])
+def test_small_weights_that_are_all_that_counts(mq, D, G, nq, Hk, page, room, below):
+    """One key has nearly all the weight and a value of zero; the others, at 2^-16 and 2^-26 of it, make the result.
+
+    A weight is held times 2^10 or more, and in the kernel of few rows times a scale of 2^-3 or more (values that differ
+    by little, an exponent above theirs): 2^-19, off by 2^-25 at most, 2^-6 of itself.  The large score, 18 in natural units,
+    is off by 2^-11 of the sum of its terms, which are of one sign: 2^-6.8.  All values point one way."""
+    rng = np.random.default_rng(58)
+    L = nq + 250
+    k, v, q = sequence(rng, L, nq, G * Hk, Hk, D, {2: below * np.log(2.0)})
+    k[np.arange(L) != 2] *= np.float32(1 / 64)
+    v = kv.bf16(rng.standard_normal(D) * (1 + 0.1 * v))
+    v[2] = 0
+    c = Cached([(kv.bf16(k), v, q)], page, room)
+    got, _ = c.run(mq)
+    K, V = kv.decode(c.cache, page, D)
+    ref, _, _ = kv.attend(c.q.astype(np.float64), K, V, c.tables, c.kv_lens, c.cu, c.scale, 0, np.zeros(c.q.shape))
+    err = np.linalg.norm(got.double().cpu().numpy() - ref, axis=-1) / np.linalg.norm(ref, axis=-1)
+    assert (err <= 2.0 ** -6 + 2.0 ** -6.8 + 2.0 ** -8).all(), err.max()
