@@ -690,8 +690,10 @@ def macaq_kv4_gather(cache: torch.Tensor, head_dim: int, page_size: int, slots: 
     (int64 [T]); zeros for negative slots."""
     pages, Hk = _need_cache(cache, page_size, head_dim)
     dev = cache.device
+    _need(slots, "slots", torch.int64, device=dev)
     T = slots.numel()
-    _need(slots, "slots", torch.int64, (T,), device=dev)
+    if slots.dim() != 1:
+        raise ValueError(f"slots must have shape ({T},), got {tuple(slots.shape)}")
     k = _out(k, "k", (T, Hk, head_dim), cache, stream)
     v = _out(v, "v", (T, Hk, head_dim), cache, stream)
     with _device(dev):

@@ -228,3 +228,11 @@ def test_padding_rows_need_no_position(mq, T, Hq, Hk, D, R, inter):
     real = np.flatnonzero(slots >= 0)
     kv.store(want, slots[real], page, kv.norm_rope(h[real, Hq:Hq + Hk], None, EPS, table[pos[real]], R, inter), h[real, Hq + Hk:])
     assert np.array_equal(cache.cpu().numpy(), want)
+
+
+def test_gather_refuses_slots_that_are_no_row_of_int64(mq):
+    cache = torch.zeros(2, 1, mq.kv4_page_bytes(16, 64), dtype=torch.uint8, device="cuda")
+    for slots in ([0, 1], torch.zeros(2, dtype=torch.int64), torch.zeros(2, dtype=torch.int32, device="cuda"),
+                  torch.zeros(1, 2, dtype=torch.int64, device="cuda")):
+        with pytest.raises(ValueError, match="slots must"):
+            mq.macaq_kv4_gather(cache, 64, 16, slots)
