@@ -423,7 +423,7 @@ int macaq_kv4_gather(const uint8_t* cache, int64_t num_pages, int page_size, int
  *                 split, so one far too large costs time).  A longer sequence's rows past it are not
  *                 written (MACAQ_EINDEX)
  *   scale    in   finite and > 0;  window in: 0, or the number of newest keys a query sees, its own included
- *   out      out  bf16 [T][Hq][D]; rows outside every sequence are left as they were
+ *   out      out  bf16 [T][Hq][D], not overlapping q; rows outside every sequence are left as they were
  *   lse      out  fp32 [T][Hq], the natural logarithm of the sum of exp(scale q k); NULL: not wanted
  *   workspace in  macaq_kv4_attention_workspace_bytes(...) bytes; contents on entry and on return
  *                 unspecified; calls sharing it must be stream-ordered

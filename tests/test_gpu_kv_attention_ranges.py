@@ -234,3 +234,30 @@ def test_kernels_that_follow_one_another_share_their_buffers(mq, nq):
     got = [call(*calls[i]) for i in order]
     assert all(torch.equal(out, want[i]) for i, out in zip(order, got))
     assert mq.macaq_device_status() == 0
+
+
+def test_more_units_than_a_cta_tells_apart(mq):
+    """Hundreds of thousands of short sequences in the kernel of many rows, some with values far apart, one to three
+    pages for all of them: every row is one of three results."""
+    rng = np.random.default_rng(43)
+    D, page, B, L = 64, 16, 330_000, 5
+    q = kv.bf16(rng.standard_normal(D))
+    cache = np.zeros((3, 1, kv.page_bytes(page, D)), np.uint8)
+    for pg in range(3):
+        k, v = kv.bf16(rng.standard_normal((2, L, 1, D)))
+        if pg == 2:
+            v[1] *= np.float32(2.0 ** 40)
+            k[1] = -8 * q  # of no weight
+        kv.store(cache, pg * page + np.arange(L), page, k, kv.bf16(v))
+    which = rng.integers(0, 2, B).astype(np.int32)
+    which[[5, 3000, 100_001, B - 1]] = 2
+    which[B // 2::977] = 2
+    K, V = kv.decode(cache, page, D)
+    want = np.stack([kv.attend(q[None, None].astype(np.float64), K, V, np.array([[pg]]), [L], [0, 1], D ** -0.5, 0,
+                               np.zeros((1, 1, D)))[0][0, 0] for pg in range(3)])
+    out = mq.macaq_kv4_attention(cuda(q, torch.bfloat16).expand(B, 1, D).contiguous(), cuda(cache), page, cuda(which[:, None]),
+                                 cuda(np.full(B, L, np.int32)), cuda(np.arange(B + 1, dtype=np.int32)), max_q=40)
+    ref = cuda(want)[cuda(which).long()]
+    err = (out[:, 0].double() - ref).norm(dim=1) / ref.norm(dim=1)
+    assert err.max() <= 5e-3
+    assert mq.macaq_device_status() == 0
