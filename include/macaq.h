@@ -427,17 +427,18 @@ int macaq_kv4_gather(const uint8_t* cache, int64_t num_pages, int page_size, int
  *   lse      out  fp32 [T][Hq], the natural logarithm of the sum of exp(scale q k); NULL: not wanted
  *   workspace in  macaq_kv4_attention_workspace_bytes(...) bytes; contents on entry and on return
  *                 unspecified; calls sharing it must be stream-ordered
- * Head h reads kv head h / (Hq / Hk).  Query i sees keys j <= its position, and with a window those
- * above position - window; a query that sees none (kv_len 0, or fewer keys than queries) gets
- * zeros and lse -inf.  Softmax statistics and sums are fp32.  Results do not depend on what the pages
- * hold behind a sequence's length, and are the same from run to run.  Rounded to f16 on the way (2^-11): the
- * transformed query, relative to its row's largest element (bits are lost below 2^-26 of it), and the softmax
- * weights.  Values may lie as far apart as they like, seen by a row or not: where a unit of work (a kv head of a
- * sequence and a tile of its query rows) meets V scales more than 2^11 (2^16 with many rows) apart, it is done again with weights as
- * sums of two bf16, which takes 2 to 3 times as long; values then count down to 2^-196 of the largest of the same
- * 32 elements.  Keys likewise; in the kernel of many query rows, blocks of a key below 2^-26 (2^-10 beside keys 2^16 times as
- * large) of its own largest block count as zero.  An infinity or NaN is stored as values of some 2^126: rows that may not
- * see it are not changed by it, one that sees such a key may be NaN.
+ * Head h reads kv head h / (Hq / Hk).  Query i sees keys j <= its position, and with a window those above
+ * position - window; a query that sees none (kv_len 0, or fewer keys than queries) gets zeros and lse -inf.
+ * Softmax statistics and sums are fp32.  Results do not depend on what the pages hold behind a sequence's
+ * length, and are the same from run to run.  Rounded to f16 on the way (2^-11): the transformed query,
+ * relative to its row's largest element (bits are lost below 2^-26 of it), and the softmax weights.  Values
+ * may lie as far apart as they like, seen by a row or not: where a unit of work (a kv head of a sequence and
+ * a tile of its query rows) meets V scales more than 2^11 (2^16 with many rows) apart or scores of 2^23, it
+ * is done again with weights as sums of two bf16, which takes 2 to 3 times as long; values then count down
+ * to 2^-196 of the largest of the same 32 elements.  Keys likewise; in the kernel of many query rows, blocks
+ * of a key below 2^-26 (2^-10 beside keys 2^16 times as large) of its own largest block count as zero.  An
+ * infinity or NaN is stored as values of some 2^126: rows that may not see it are not changed by it, one
+ * that sees such a key may be NaN.
  */
 size_t macaq_kv4_attention_workspace_bytes(int64_t T, int64_t B, int Hq, int Hk, int head_dim, int64_t max_q);
 int macaq_kv4_attention(const uint16_t* q, int64_t T, int64_t ldq, int Hq, int Hk, int head_dim,

@@ -257,6 +257,13 @@ __device__ __forceinline__ float warp_fwht32(float x, int l) {
 constexpr float kSlack = 5.0f;
 constexpr float kLift = 10.0f;
 
+// A weight's exponent is fma(product, factor, -reference), with the reference made of the largest score rounded to fp32:
+// for scores of 2^24 and more that rounding could be the whole exponent.  Where a row's last reference is this large, the
+// unit is done again (WIDE), with scores that are rounded before the reference is taken from them.  (Infinite: a row
+// that is NaN.)  Sums relative to earlier references as large are wiped when the reference moves on.
+__device__ __forceinline__ bool too_large(float ref) { return fabsf(ref) >= 8388608.0f && fabsf(ref) < INFINITY; }
+__device__ __forceinline__ float rescaled(float x, float by) { return by == 0.0f ? 0.0f : x * by; }  // x may be infinite
+
 // Where V's scales lie too far apart for f16, weights times scales are bf16, whose exponents are fp32's, relative to
 // a reference 2^70 below the largest scale of the same 32 elements: 2^70, times 6, a weight of 2^15 and 2^30 keys, stays
 // below 2^118, and scales down to 2^-196 of the largest are not lost beside it (an infinity is stored as 2^126, so values
@@ -615,11 +622,11 @@ __device__ __forceinline__ bool few_unit(const AttendParams& p, FewShared<D, NT>
                             ref[n][e] = m - kLift;
                             const float shift = bound[n][e] == -INFINITY ? 0.0f : exp2_approx(old - ref[n][e]);
                             bound[n][e] = m + kSlack;
-                            sum[n][e] *= shift;
+                            sum[n][e] = rescaled(sum[n][e], shift);
                             scale *= shift;
                         }
 #pragma unroll
-                        for (int x = 0; x < 2 * kBlocks; ++x) o[n][x][e] *= scale, o[n][x][2 + e] *= scale;
+                        for (int x = 0; x < 2 * kBlocks; ++x) o[n][x][e] = rescaled(o[n][x][e], scale), o[n][x][2 + e] = rescaled(o[n][x][2 + e], scale);
                     }
                 }
             }
@@ -639,10 +646,18 @@ __device__ __forceinline__ bool few_unit(const AttendParams& p, FewShared<D, NT>
                 uint32_t pt0[NT], pt1[NT], pl0[NT], pl1[NT];  // (pl: what bf16 leaves of the weights)
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
-                    const float e0 = exp2_approx(fmaf(sc[u][n][0], f[n][0], -ref[n][0]));
-                    const float e1 = exp2_approx(fmaf(sc[u][n][1], f[n][1], -ref[n][1]));
-                    const float e2 = exp2_approx(fmaf(sc[u][n][2], f[n][0], -ref[n][0]));
-                    const float e3 = exp2_approx(fmaf(sc[u][n][3], f[n][1], -ref[n][1]));
+                    float e0, e1, e2, e3;
+                    if constexpr (WIDE) {
+                        e0 = exp2_approx(__fsub_rn(__fmul_rn(sc[u][n][0], f[n][0]), ref[n][0]));
+                        e1 = exp2_approx(__fsub_rn(__fmul_rn(sc[u][n][1], f[n][1]), ref[n][1]));
+                        e2 = exp2_approx(__fsub_rn(__fmul_rn(sc[u][n][2], f[n][0]), ref[n][0]));
+                        e3 = exp2_approx(__fsub_rn(__fmul_rn(sc[u][n][3], f[n][1]), ref[n][1]));
+                    } else {
+                        e0 = exp2_approx(fmaf(sc[u][n][0], f[n][0], -ref[n][0]));
+                        e1 = exp2_approx(fmaf(sc[u][n][1], f[n][1], -ref[n][1]));
+                        e2 = exp2_approx(fmaf(sc[u][n][2], f[n][0], -ref[n][0]));
+                        e3 = exp2_approx(fmaf(sc[u][n][3], f[n][1], -ref[n][1]));
+                    }
                     sum[n][0] += e0 + e2, sum[n][1] += e1 + e3;
                     if constexpr (WIDE) {
                         const uint32_t a = pack_bf16(e0, e1), z = pack_bf16(e2, e3);
@@ -751,7 +766,13 @@ __device__ __forceinline__ bool few_unit(const AttendParams& p, FewShared<D, NT>
             }
         }
         if (lane < kBlocks) sm.vref[warp][lane] = __uint_as_float(static_cast<uint32_t>(vref) << 23);
-        __syncthreads();
+        if constexpr (WIDE) {
+            __syncthreads();
+        } else if (__syncthreads_or(too_large(ref[n][0]) || too_large(ref[n][1]))) {
+            if (lane < kBlocks) sm.vtop[warp][lane] = vref;  // above the largest of all blocks
+            __syncwarp();
+            return false;
+        }
         constexpr int kAtOnce = kFewThreads / D;
         const int d = threadIdx.x % D;
 #pragma unroll
@@ -845,7 +866,8 @@ static_assert(2 * kSoftmaxRegs + 2 * kCodeRegs + kIssueRegs <= 5 * kManyLaunchRe
 constexpr int kOperandLift = 12;
 constexpr int kManyUnits = 4, kUnitReaders = 18;
 constexpr int kManySpan = 16;
-constexpr int kRedoUnits = 2048;     // units of a CTA that are told apart (of those behind, all are done again or none)
+constexpr int kRedoUnits = 2048;  // units of a CTA that are told apart (of those behind, all are done again or none)
+static_assert(kRedoUnits / 4 + 1 <= kManyThreads, "one word a thread");
 // WIDE, a column's factor is 2^(its token's largest scale - kKeyReference): 2^60 for an infinity's, where products reach 2^38
 constexpr int kKeyReference = 193;
 
@@ -871,9 +893,8 @@ struct ManyShared {
     uint32_t tmem;
     PlaceShared place;
     Place start;  // the CTA's range
-    // units (by their number in the range) whose scales lie too far apart: written by one warp; `redo_all`: from that on
-    uint32_t redo[kRedoUnits / 32];
-    int redo_any, redo_all;
+    alignas(4) uint8_t redo[kRedoUnits + 4];  // units (by their number in the range) to be done again
+    int redo_any;
     // the CTA's units in order, written by one warp (so that no other spends registers on finding them) and read
     // by the 18 that work on them; past the last one stands an empty one
     Unit unit[kManyUnits];
@@ -911,8 +932,13 @@ __device__ __forceinline__ bool next_unit(ManyShared<D>& sm, int n, int lane) {
 }
 
 template <int D>
+__device__ __forceinline__ void mark_redo(ManyShared<D>& sm, int n) {
+    sm.redo[min(n, kRedoUnits)] = 1;
+    sm.redo_any = 1;
+}
+template <int D>
 __device__ __forceinline__ bool must_redo(const ManyShared<D>& sm, int n) {
-    return n < kRedoUnits ? sm.redo[n >> 5] >> (n & 31) & 1u : sm.redo_all != 0;
+    return sm.redo[min(n, kRedoUnits)] != 0;
 }
 
 // One warp: writes the units (WIDE: those that are done again).
@@ -1018,13 +1044,7 @@ __device__ __forceinline__ void many_ranges(const AttendParams& p, ManyShared<D>
             return static_cast<int>(__reduce_max_sync(0xFFFFFFFFu, max(top & 0xFFFFu, top >> 16))) -
                    static_cast<int>(__reduce_min_sync(0xFFFFFFFFu, min(low & 0xFFFFu, low >> 16))) - 1;
         };
-        if (max(span(vtop, vlow), span(ktop, klow)) > kManySpan && lane == 0) {
-            sm.redo_any = 1;
-            if (n < kRedoUnits)
-                sm.redo[n >> 5] |= 1u << (n & 31);
-            else
-                sm.redo_all = 1;
-        }
+        if (max(span(vtop, vlow), span(ktop, klow)) > kManySpan && lane == 0) mark_redo<D>(sm, n);
     }
 }
 
@@ -1493,6 +1513,7 @@ __device__ __forceinline__ void many_softmax(const AttendParams& p, ManyShared<D
                 }
             }
             tc_fence_before();
+            if (!WIDE && __any_sync(0xFFFFFFFFu, too_large(m))) mark_redo<D>(sm, units - 1);
             if (out >= 0) {
                 if (out_slot >= 0)
                     p.part_ml[at] = make_float2(m, sum);
@@ -1567,7 +1588,7 @@ __device__ __forceinline__ void many_softmax(const AttendParams& p, ManyShared<D
                     ref = m - kLift;
                     const float shift = bound == -INFINITY ? 0.0f : exp2_approx(old - ref);
                     bound = m + kSlack;
-                    sum *= shift;
+                    sum = rescaled(sum, shift);
                     scale *= shift;
                 }
                 if (h > 0) {  // once the products of the half before are done (those of halves before that are: s_full)
@@ -1585,7 +1606,7 @@ __device__ __forceinline__ void many_softmax(const AttendParams& p, ManyShared<D
                             more = __uint_as_float(static_cast<uint32_t>(127 - (d - d / 2)) << 23);
                         }
 #pragma unroll
-                        for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * by * more);
+                        for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(rescaled(__uint_as_float(o[k]), by) * more);
                         tmem_st16(to + 16 * i, o);
                     }
                 }
@@ -1598,7 +1619,11 @@ __device__ __forceinline__ void many_softmax(const AttendParams& p, ManyShared<D
                 uint32_t w[16], rest[16];
 #pragma unroll
                 for (int k = 0; k < 16; ++k) {
-                    float2 e = __ffma2_rn(make_float2(s[32 * i + 2 * k], s[32 * i + 2 * k + 1]), f2, r2);
+                    float2 e = make_float2(s[32 * i + 2 * k], s[32 * i + 2 * k + 1]);
+                    if constexpr (WIDE)  // (the packed operations would be fused)
+                        e = make_float2(__fsub_rn(__fmul_rn(e.x, f[i]), ref), __fsub_rn(__fmul_rn(e.y, f[i]), ref));
+                    else
+                        e = __ffma2_rn(e, f2, r2);
                     e = make_float2(exp2_approx(e.x), exp2_approx(e.y));
                     add[k & 1] = __fadd2_rn(add[k & 1], e);
                     if constexpr (WIDE) {
@@ -1677,9 +1702,9 @@ __global__ void __launch_bounds__(kManyThreads, 1) attend_many_kernel(const __gr
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     if (threadIdx.x == 0) {
         many_init(sm, false, kUnitReaders + 1);  // and the warp that looks at the scales
-        sm.abort = 0, sm.redo_any = 0, sm.redo_all = 0;
+        sm.abort = 0, sm.redo_any = 0;
     }
-    if (threadIdx.x < kRedoUnits / 32) sm.redo[threadIdx.x] = 0;
+    if (threadIdx.x < sizeof(sm.redo) / 4) reinterpret_cast<uint32_t*>(sm.redo)[threadIdx.x] = 0;
     if (warp == 16) {
         tmem_alloc(&sm.tmem, 512);
         tmem_relinquish();

@@ -217,3 +217,47 @@ def test_small_weights_that_are_all_that_counts(mq, D, G, nq, Hk, page, room, be
     ref, _, _ = kv.attend(c.q.astype(np.float64), K, V, c.tables, c.kv_lens, c.cu, c.scale, 0, np.zeros(c.q.shape))
     err = np.linalg.norm(got.double().cpu().numpy() - ref, axis=-1) / np.linalg.norm(ref, axis=-1)
     assert (err <= 2.0 ** -6 + 2.0 ** -6.8 + 2.0 ** -8).all(), err.max()
+
+
+@pytest.mark.parametrize("D,G,nq,Hk,page,room", KERNELS)
+@pytest.mark.parametrize("gain", [2.0 ** 22, 2.0 ** 27, 2.0 ** 40, 2.0 ** 70])
+def test_scores_beyond_the_steps_of_fp32(mq, D, G, nq, Hk, page, room, gain):
+    """The newest key's score is some 2^22 to 2^70, of one sign for even heads and of the other for odd ones: it has all the
+    weight, or none.  The newest query's result is that key's value, within its rounding and that of the sums, or what the
+    other keys make, as in any other test."""
+    rng = np.random.default_rng(59)
+    L = nq + 60
+    k, v, q = sequence(rng, L, nq, G * Hk, Hk, D)
+    u = kv.bf16(rng.standard_normal(D))
+    q[-1] = u * np.where(np.arange(G * Hk) % 2, -1, 1)[:, None]
+    k[-1] = kv.bf16(u * np.float32(gain))
+    c = Cached([(k, v, q)], page, room)
+    c.check(mq, earlier)
+    got = c.run(mq)[0].double().cpu().numpy()[-1]
+    assert np.isfinite(got).all()
+    K, V = kv.decode(c.cache, page, D)
+    j = np.arange(L)
+    vs = V[c.tables[0][j // page], :, j % page]
+    for h in range(0, G * Hk, 2):
+        ref = vs[-1, h // G]
+        size = np.abs(ref).reshape(-1, 32).sum(-1).repeat(32)
+        assert (np.abs(got[h] - ref) <= 2.0 ** -8 * np.abs(ref) + (L + 64) * 2.0 ** -24 * size + 2.0 ** -10 * size / 32).all()
+    ks = K[c.tables[0][j // page], :, j % page]
+    for h in range(1, G * Hk, 2):
+        s = ks[:-1, h // G] @ c.q[-1, h].astype(np.float64) * c.scale
+        p = np.exp(s - s.max())
+        ref = p / p.sum() @ vs[:-1, h // G]
+        assert np.linalg.norm(got[h] - ref) <= 0.01 * np.linalg.norm(ref)
+
+
+@pytest.mark.parametrize("D,G,nq,Hk,page,room", KERNELS)
+@pytest.mark.parametrize("gain", [2.0 ** 27, 2.0 ** 50])
+def test_ordinary_scores_behind_huge_negative_ones(mq, D, G, nq, Hk, page, room, gain):
+    """What a row has summed relative to a reference of -2^27 and below is gone without a trace when its first ordinary
+    score comes; rows that see the huge ones alone have those."""
+    rng = np.random.default_rng(62)
+    L = nq + 200
+    k, v, q = sequence(rng, L, nq, G * Hk, Hk, D, {j: 2.0 * np.sin(j) for j in range(150, L)})
+    k[:150] = -np.sign(q[0, 0]) * np.abs(k[:150]) * np.float32(gain)
+    c = Cached([(kv.bf16(k), v, q)], page, room)
+    c.check(mq)
