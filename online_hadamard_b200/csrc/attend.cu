@@ -339,7 +339,8 @@ struct FewShared {
     PlaceShared place;
 };
 
-// One unit, or a CTA's part of it.  False, and nothing written, where V's scales lie too far apart for f16 (not WIDE).
+// One unit, or a CTA's part of it.  False where it is to be done again, WIDE: V's scales lie too far apart for f16, or
+// scores are too large (results of some of its rows may have been written then).
 template <int D, int NT, bool WIDE>
 __device__ __forceinline__ bool few_unit(const AttendParams& p, FewShared<D, NT>& sm, const Unit& unit) {
     const Sequence& s = unit.t.s;
@@ -853,7 +854,8 @@ __global__ void __launch_bounds__(kFewThreads, few_resident(NT)) attend_few_kern
 //
 // Measured: a prompt of 8192 tokens, 32 heads of 128 on 8, 639 us with the joining kernel in a captured graph, 860 TFLOP/s
 // of the pairs the mask leaves (tensor pipe less than half busy); the public call takes 640 to 680 us.  When this kernel
-// alone took 605 us, neither the exponentials (replaced by a product: 583 us) nor the widening (left out: 577 us) bound it, but the chain scores - maximum - weights - products of a tile with only two softmax warps a scheduler to hide it.
+// alone took 605 us, neither the exponentials (replaced by a product: 583 us) nor the widening (left out: 577 us) bound it,
+// but the chain scores - maximum - weights - products of a tile with only two softmax warps a scheduler to hide it.
 // On the way there: products issued by a thread that the compiler did not know to be one 1713 us, by a converged
 // warp 1310; code cut so that the roles' loops fit the instruction cache 718; scores of half blocks ahead, two issuing
 // warps 640.  Letting the two tiles' exponentials take turns cost 3 %.
@@ -1026,11 +1028,11 @@ __device__ __forceinline__ void many_ranges(const AttendParams& p, ManyShared<D>
         for (int t = from; t <= last; t += 32 * kTokens) {
             const uint8_t* at = scales(t);
             if (!at) continue;
-#pragma unroll 1
+            const uint4 k4 = __ldcg(reinterpret_cast<const uint4*>(at)), v4 = __ldcg(reinterpret_cast<const uint4*>(at + v_at));
+#pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const uint32_t see = mask(t, i);
-                const uint32_t k = __ldcg(reinterpret_cast<const uint32_t*>(at) + i) & see;
-                const uint32_t v = __ldcg(reinterpret_cast<const uint32_t*>(at + v_at) + i) & see;
+                const uint32_t k = reinterpret_cast<const uint32_t*>(&k4)[i] & see, v = reinterpret_cast<const uint32_t*>(&v4)[i] & see;
                 const uint32_t ve = v & 0x00FF00FFu, vo = v >> 8 & 0x00FF00FFu;
                 vtop = __vmaxu2(vtop, __vmaxu2(ve, vo));
                 vlow = __viaddmin_u16x2(vo, 0xFFFFFFFFu, __viaddmin_u16x2(ve, 0xFFFFFFFFu, vlow));
