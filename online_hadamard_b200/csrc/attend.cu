@@ -281,8 +281,8 @@ __device__ __forceinline__ int wide_reference(int top) { return max(top - 70, 1)
 // until the end, where the warps' sums are joined.
 //
 // Measured (heads of 128, 64 on 8; the kernel and the joining one, in a captured graph): 16 sequences of 32768 keys, 570 MB
-// of cache, 121 us, 4.7 TB/s; 32 on 8, 32 sequences of up to 8000 keys (157 MB), 47 us, 3.3 TB/s.  The public call takes
-// 121 to 133 and 45 to 49 us.  A strip of 16 tokens takes about 284 warp
+// of cache, 124 us, 4.6 TB/s; 32 on 8, 32 sequences of up to 8000 keys (157 MB), 48 us, 3.3 TB/s.  The public call takes
+// 121 to 135 and 45 to 49 us.  A strip of 16 tokens takes about 284 warp
 // instructions (a conversion per two codes, 64, and 32 matrix instructions and their scales among them); they fill 56 %
 // of the issue slots of three CTAs an SM.  Four CTAs (128 registers, spilling) issue no more; one strip at a time
 // is 9 % slower, as two in flight hide each other's latencies; a CTA's start and end cost some 15 us in all.
@@ -852,7 +852,7 @@ __global__ void __launch_bounds__(kFewThreads, few_resident(NT)) attend_few_kern
 // as long that way, 2.8 times in all (prompt of 8192 tokens, a value 2^40 times larger in each head: 0.64 / 1.8 ms).  A
 // branch in the roles' loops instead, or the look at the scales in the role that widens V, cost every call 15 % and more.
 //
-// Measured: a prompt of 8192 tokens, 32 heads of 128 on 8, 639 us with the joining kernel in a captured graph, 860 TFLOP/s
+// Measured: a prompt of 8192 tokens, 32 heads of 128 on 8, 629 us with the joining kernel in a captured graph, 875 TFLOP/s
 // of the pairs the mask leaves (tensor pipe less than half busy); the public call takes 640 to 680 us.  When this kernel
 // alone took 605 us, neither the exponentials (replaced by a product: 583 us) nor the widening (left out: 577 us) bound it,
 // but the chain scores - maximum - weights - products of a tile with only two softmax warps a scheduler to hide it.
